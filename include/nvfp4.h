@@ -404,6 +404,137 @@ int nvfp4_select_route(int64_t M, int64_t K, int64_t N, int transpose,
  * only); with K % 256 == 0 it goes up to 64. */
 int64_t nvfp4_qmv_max_rows(void);
 
+/*
+ * Serving operators around the quantized products: a paged key/value cache
+ * held in 8 bits, attention over it, and the choice of the next token.
+ *
+ * The cache is a pool of pages of `page` tokens each.  A sequence's page i,
+ * its tokens [i * page, (i + 1) * page), is page table[b, i] of the pool; an
+ * entry outside [0, pages) is a page that is not there.
+ *
+ *   k         uint8 [pages, heads, page, dim]   E4M3 codes of the keys
+ *   v         uint8 [pages, heads, dim, page]   E4M3 codes of the values
+ *   k_scales  uint8 [pages, heads]              power-of-two scales, exponent + 127
+ *   v_scales  uint8 [pages, heads]
+ *
+ * A value is its code times 2^(scale - 127).  page is 16, 32, 64, 128 or 256;
+ * dim is 64, 128, 192 or 256; k and v are 16-byte aligned.  Values lie with a
+ * channel's tokens side by side, the order in which the product of weights
+ * and values reads them.
+ *
+ * Sequences: lens[b] int32 is the number of tokens of sequence b, the new
+ * ones (the last of them) among them.  The new tokens of all sequences lie
+ * one after the other in rows [cu_q[b], cu_q[b + 1]) of q, k and v, with
+ * cu_q int32 [batch + 1] from 0 to `tokens`; with cu_q NULL every sequence
+ * has one new token and tokens == batch.  max_q is an upper bound of the new
+ * tokens of a sequence that sizes the launch; it does not change a result.
+ * Tensors of tokens are [tokens, heads, dim] with the last axis contiguous
+ * and any strides (in elements, >= 0) of the other two.
+ *
+ * These values live on the device and are not read on the host.  The kernels
+ * stay inside the buffers whatever they hold: rows outside [0, tokens) and
+ * pages that are not there are left out.
+ */
+typedef struct nvfp4_kv_cache {
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* k_scales;
+  uint8_t* v_scales;
+  int64_t pages, heads, page, dim;
+} nvfp4_kv_cache_t;
+
+/*
+ * nvfp4_kv_append -- rotates the new keys by their positions, quantizes the
+ * new keys and values and writes both into the cache; rotates the new
+ * queries into q_out.
+ *
+ *   k, v    [tokens, heads, dim] of dtype, strides k_token, k_head, v_token,
+ *           v_head
+ *   q       [tokens, heads_q, dim] of dtype, strides q_token, q_head, or NULL
+ *           (then q_out is NULL too)
+ *   q_out   [tokens, heads_q, dim] of dtype, contiguous, 16-byte aligned
+ *   inv_freq float [rot / 2] or NULL with rot 0: channels [0, rot) (rot even,
+ *           at most dim) of token position p turn by the angles p * inv_freq[i].
+ *           The pair i is channels (i, i + rot / 2), or (2i, 2i + 1) with
+ *           interleaved != 0.
+ *
+ * A page's scale of a head and side is the smallest power of two p with
+ * amax <= 448 p over the finite new values that the call writes into it, or
+ * the page's present scale if that is larger and the page holds earlier
+ * tokens of the sequence, whose codes are then rounded anew at the grown
+ * scale.  Values that are not finite become NaN codes.  Codes behind a
+ * sequence's last token keep what they held.  The angles are formed and
+ * reduced in 64 bits, so far positions lose nothing; each value is rounded
+ * to 32 bits after its rotation and then once to its code, or to q_out.
+ * Pages that a call writes must belong to one sequence each.
+ */
+int nvfp4_kv_append(const nvfp4_kv_cache_t* cache, const void* k, int64_t k_token, int64_t k_head,
+                    const void* v, int64_t v_token, int64_t v_head, const void* q, int64_t q_token,
+                    int64_t q_head, int64_t heads_q, void* q_out, nvfp4_dtype_t dtype, int64_t tokens,
+                    const int32_t* cu_q, int64_t batch, int64_t max_q, const int32_t* table,
+                    int64_t table_width, const int32_t* lens, const float* inv_freq, int64_t rot,
+                    int interleaved, hipStream_t stream);
+
+/*
+ * nvfp4_paged_attention -- attention of the new tokens over the cached ones.
+ *
+ *   q    [tokens, heads_q, dim] of dtype, strides q_token, q_head; heads_q is
+ *        a multiple of cache->heads (query head h reads head h / (heads_q /
+ *        heads))
+ *   out  [tokens, heads_q, dim] of dtype, contiguous, 16-byte aligned
+ *
+ * The query of position p sees the cached tokens t <= p, with window > 0
+ * only those with t > p - window, as far as their pages are there:
+ *   out = sum_t softmax_t(scale * q . k_t) v_t
+ * and zeros where it sees none.  Tokens that it does not see have no effect,
+ * NaN codes among them included.  Products and sums are in 32 bits; weights
+ * are rounded to the 2-byte dtype for their product with the values (float32:
+ * to three bf16 parts, exactly).
+ *
+ * workspace (device, 16-byte aligned, of at least
+ * nvfp4_paged_attention_workspace_size bytes) holds the partial results of a
+ * long axis that is split; without it the axis is not split.
+ */
+int64_t nvfp4_paged_attention_workspace_size(int64_t tokens, int64_t heads_q, int64_t heads, int64_t dim,
+                                             int64_t page, int64_t batch, int64_t max_q,
+                                             int64_t table_width, int64_t window, nvfp4_dtype_t dtype);
+int nvfp4_paged_attention(const nvfp4_kv_cache_t* cache, const void* q, int64_t q_token, int64_t q_head,
+                          int64_t heads_q, nvfp4_dtype_t dtype, int64_t tokens, const int32_t* cu_q,
+                          int64_t batch, int64_t max_q, const int32_t* table, int64_t table_width,
+                          const int32_t* lens, int64_t window, float scale, void* workspace,
+                          int64_t workspace_bytes, void* out, hipStream_t stream);
+
+/*
+ * nvfp4_sample -- one token per row from its logits and a given random number.
+ *
+ *   logits       [batch, vocab] of dtype, row stride row_stride (elements)
+ *   u            float [batch], in [0, 1)
+ *   temperature  float [batch] or NULL (1)
+ *   top_k        int32 [batch] or NULL; <= 0 keeps all
+ *   top_p, min_p float [batch] or NULL; 1 and 0 keep all
+ *   token        int32 [batch]
+ *   prob         float [batch] or NULL: the token's probability among the kept
+ *
+ * The tokens are ordered by falling logit, equal ones by rising index; w =
+ * exp((logit - largest) / temperature).  top_k keeps the first k of them;
+ * top_p those of these that have less than top_p of the first k's sum of w
+ * before them; min_p those with w >= min_p; the first one always stays.  The
+ * result is the first kept token, by index, whose running sum of w exceeds u
+ * times the kept ones' sum.  NaN logits count as -inf; a row with nothing
+ * above -inf gives token -1 and probability 0.  Weights and sums are in 64
+ * bits (the sums that place the top_p border in 62-bit fixed point), added in
+ * a fixed order: results repeat bit for bit.
+ *
+ * workspace (device, 16-byte aligned, of at least
+ * nvfp4_sample_workspace_size bytes) lets several blocks share a row;
+ * without it each row runs in one block.
+ */
+int64_t nvfp4_sample_workspace_size(int64_t batch, int64_t vocab, nvfp4_dtype_t dtype);
+int nvfp4_sample(const void* logits, nvfp4_dtype_t dtype, int64_t batch, int64_t vocab, int64_t row_stride,
+                 const float* u, const float* temperature, const int32_t* top_k, const float* top_p,
+                 const float* min_p, void* workspace, int64_t workspace_bytes, int32_t* token, float* prob,
+                 hipStream_t stream);
+
 /* Human-readable text for a status code (host only; static storage). */
 const char* nvfp4_status_string(int status);
 

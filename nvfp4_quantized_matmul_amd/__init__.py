@@ -25,6 +25,7 @@ __all__ = [
     "NVFP4Error", "library_path", "load_library", "transcode", "dequantize", "quantize", "qmm",
     "qmm_batched", "qmm_glu", "gather_qmm", "select_route", "qmv_max_rows", "status_string",
     "ROUTE_AUTO", "ROUTE_QMV", "ROUTE_GEMM", "GLU_ACTIVATIONS",
+    "KVCache", "kv_append", "paged_attention", "sample",
 ]
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -79,6 +80,13 @@ def load_library() -> ctypes.CDLL:
         "nvfp4_qmm_glu": [vp, c_int, i64, i64, i64, vp, vp, vp, vp, vp, vp, c_int, vp, i64, vp, vp],
         "nvfp4_qmm_glu_workspace_size": [i64, i64, i64, c_int],
         "nvfp4_gather_qmm": [vp, c_int, i64, i64, i64, vp, vp, i64, vp, vp, vp, i64, i64, c_int, vp, vp],
+        "nvfp4_kv_append": [vp, vp, i64, i64, vp, i64, i64, vp, i64, i64, i64, vp, c_int, i64, vp, i64, i64, vp, i64,
+                            vp, vp, i64, c_int, vp],
+        "nvfp4_paged_attention_workspace_size": [i64] * 9 + [c_int],
+        "nvfp4_paged_attention": [vp, vp, i64, i64, i64, c_int, i64, vp, i64, i64, vp, i64, vp, i64, ctypes.c_float,
+                                  vp, i64, vp, vp],
+        "nvfp4_sample_workspace_size": [i64, i64, c_int],
+        "nvfp4_sample": [vp, c_int, i64, i64, i64, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp],
         "nvfp4_select_route": [i64, i64, i64, c_int, c_int],
         "nvfp4_qmv_max_rows": [],
         "nvfp4_status_string": [c_int],
@@ -92,6 +100,8 @@ def load_library() -> ctypes.CDLL:
     lib.nvfp4_qmm_workspace_size.restype = i64
     lib.nvfp4_qmm_glu_workspace_size.restype = i64
     lib.nvfp4_static_scratch_bytes.restype = i64
+    lib.nvfp4_paged_attention_workspace_size.restype = i64
+    lib.nvfp4_sample_workspace_size.restype = i64
     lib.nvfp4_status_string.restype = ctypes.c_char_p
     _lib = lib
     return lib
@@ -475,3 +485,6 @@ def gather_qmm(x: torch.Tensor, w: torch.Tensor, scales: torch.Tensor,
         _ptr(x), code, X, M, K, _ptr(lhs_indices), _ptr(rhs_indices), R, _ptr(w), _ptr(scales),
         _ptr(gs), E, N, int(bool(sorted_indices)), _ptr(out), _stream(dev)))
     return out
+
+
+from .serving import KVCache, kv_append, paged_attention, sample  # noqa: E402  (needs the helpers above)

@@ -1,0 +1,685 @@
+// Attention of new tokens over the paged 8-bit key/value cache: out =
+// softmax(scale q K^T) V, one pass over the cache with a running maximum and
+// sum per query row.
+//
+// Both products run transposed on the matrix cores, S^T = K Q^T and O^T = V^T
+// P^T, with a query row per column.  A lane then holds scores of one row only,
+// so the running maximum is the lane's own; and its scores are consecutive
+// tokens of that row, the very operand that the second product takes, if the
+// 16 key rows of a multiply are taken in the right order.  Weights never leave
+// their registers.  An E4M3 code is exact in bf16 and f16, so codes are
+// converted in registers and multiply 2-byte queries; float32 queries and
+// weights multiply as three bf16 parts whose sum is the float.
+//
+// Scales.  Keys: the score of a token is multiplied by its page's power of
+// two.  Values: with s the score in powers of two and e the exponent of the
+// value scale, the weight in units of codes is 2^(s + e), so the running
+// maximum m is that of s + e, the weights 2^(s + e - m) are at most 1 in any
+// type, and the sum of the softmax takes each of them times 2^-e.
+//
+// What a row does not see gets s = -inf.  A NaN code among its values would
+// still spoil the product, as 0 * NaN: a tile that is not seen whole by all
+// rows is searched for them, and one that holds any takes a separate path.
+#include <climits>
+
+#include "kv_cache.hpp"
+#include "nvfp4_internal.hpp"
+
+namespace {
+
+using namespace nvfp4dev;
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+struct AttnArgs {
+  CacheView c;
+  SequenceView s;
+  const void* q;
+  int64_t q_token, q_head;
+  void* out;
+  float *part_o, *part_m, *part_l;   // of a split axis: [tokens * heads_q][splits][dim], twice [tokens * heads_q][splits]
+  int32_t heads_q, group;
+  int32_t window;                    // <= 0: none
+  int32_t splits, chunk;             // chunk: tokens of a split, a multiple of 64
+  int32_t row_tiles;                 // of a sequence and head, at most
+  float scale_log2;                  // scale * log2(e)
+  bool vec;                          // 16-byte loads of q
+};
+
+typedef int32_t i32x4_t __attribute__((ext_vector_type(4)));
+
+template <typename T>
+struct Mma;
+template <>
+struct Mma<__bf16> {
+  typedef __bf16 E;
+  typedef bf16x8_t V8;
+  static constexpr int kParts = 1;
+  static __device__ __forceinline__ f32x4_t mul(V8 a, V8 b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+};
+template <>
+struct Mma<float> : Mma<__bf16> {
+  static constexpr int kParts = 3;
+};
+template <>
+struct Mma<_Float16> {
+  typedef _Float16 E;
+  typedef f16x8_t V8;
+  static constexpr int kParts = 1;
+  static __device__ __forceinline__ f32x4_t mul(V8 a, V8 b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
+};
+
+// Eight codes (two words) as an operand, exactly.
+template <typename V8>
+__device__ __forceinline__ V8 decode8(uint32_t lo, uint32_t hi) {
+  uint32_t d[4];
+  if constexpr (__is_same(V8, bf16x8_t)) {
+    d[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false));
+    d[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true));
+    d[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false));
+    d[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true));
+  } else {
+    d[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false));
+    d[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true));
+    d[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false));
+    d[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true));
+  }
+  return __builtin_bit_cast(V8, d);
+}
+
+// 0x80 in each byte of w that is a NaN code.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+// 1.0 (code 0x38) where `nan` has 0x80, else 0.
+__device__ __forceinline__ uint32_t nan_ones(uint32_t nan) { return (nan >> 2) | (nan >> 3) | (nan >> 4); }
+
+// Eight floats as the parts of an operand: rounded once to a 2-byte type, or
+// split into three bf16 parts.
+template <typename T>
+__device__ __forceinline__ void to_parts(const float (&x)[8], typename Mma<T>::V8 (&p)[Mma<T>::kParts]) {
+  if constexpr (Mma<T>::kParts == 1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[0][i] = (typename Mma<T>::E)x[i];
+  } else {
+    uint32_t d[3][4];
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      uint32_t h0, m0, l0, h1, m1, l1;
+      split3_bits(fbits(x[i]), h0, m0, l0);
+      split3_bits(fbits(x[i + 1]), h1, m1, l1);
+      d[0][i / 2] = __builtin_amdgcn_perm(h1, h0, 0x07060302u);
+      d[1][i / 2] = __builtin_amdgcn_perm(m1, m0, 0x07060302u);
+      d[2][i / 2] = __builtin_amdgcn_perm(l1, l0, 0x07060302u);
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) p[k] = __builtin_bit_cast(bf16x8_t, d[k]);
+  }
+}
+
+// Eight channels of a query row from element offset 8 c on.
+template <typename T>
+__device__ __forceinline__ void load_row8(const T* row, bool vec, float (&x)[8]) {
+  if (vec) {
+    if constexpr (sizeof(T) == 4) {
+      const f32x4_t lo = *(const f32x4_t*)row, hi = *((const f32x4_t*)row + 1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) { x[i] = lo[i]; x[4 + i] = hi[i]; }
+    } else {
+      typedef T vec8 __attribute__((ext_vector_type(8)));
+      const vec8 u = *(const vec8*)row;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = (float)u[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = load_x(row + i);
+  }
+}
+
+__device__ __forceinline__ float pow2(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float max_across_groups(float v) {
+  v = fmaxf(v, __shfl_xor(v, 16, 64));
+  return fmaxf(v, __shfl_xor(v, 32, 64));
+}
+__device__ __forceinline__ float sum_across_groups(float v) {
+  v += __shfl_xor(v, 16, 64);
+  return v + __shfl_xor(v, 32, 64);
+}
+
+// The tokens that rows [t0, t1] (token numbers among the new ones) see, and
+// where a split axis starts.
+struct Span {
+  int32_t first, last;   // positions of the first and the last row
+  int32_t begin, end;    // cached tokens that any of the rows sees; begin on a tile
+};
+
+__device__ __forceinline__ Span span_of(const AttnArgs& A, const Sequence& s, int t0, int t1) {
+  Span r;
+  r.first = s.len - s.count + t0;
+  r.last = s.len - s.count + t1;
+  const int64_t cap = A.s.width << A.c.page_shift;
+  r.end = r.last + 1 < cap ? r.last + 1 : (int32_t)cap;
+  const int32_t lo = A.window > 0 && r.first >= A.window ? r.first - A.window + 1 : 0;
+  r.begin = lo & ~63;
+  return r;
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: the waves of a block share the rows and split the tokens
+// ---------------------------------------------------------------------------
+//
+// A tile is 64 tokens.  Lane (n, g) = (lane % 16, lane / 16) holds tokens 16 g
+// .. 16 g + 15 of column n, so a 16-byte load of codes is one channel's tokens
+// (values) or 16 channels of one token (keys).  Key row m of multiply t is
+// token 16 (m / 4) + 4 t + m % 4: with four rows per lane group in the result,
+// lane group g gets the tokens 16 g + 4 t + (0..3) from it.  Nothing is shared
+// between waves until the end, so K and V go straight from memory to
+// registers; the queries lie in LDS as operands.
+constexpr int kFewWaves = 4;
+
+template <int DIM, int NT, int PARTS>
+constexpr int few_lds_bytes() {
+  constexpr int q = NT * 16 * DIM * 2 * PARTS;          // operands
+  constexpr int red = 2 * NT * 16 * DIM * 4 + kFewWaves * NT * 16 * 2 * 4;  // two waves' sums; all waves' maxima and sums
+  return q > red ? q : red;
+}
+
+// Registers a lane needs for the running sums, a tile's scores and its codes:
+// past what two blocks a unit leave each, one block has them all.
+template <int DIM, int NT, int PARTS>
+constexpr int few_blocks_per_cu() { return NT * DIM / 4 + 16 * NT + DIM / 2 + 24 * PARTS * NT + 64 <= 256 ? 2 : 1; }
+
+template <typename T, int DIM, int NT>
+__global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>::kParts>())) void few_rows_kernel(AttnArgs A) {
+  typedef Mma<T> M;
+  typedef typename M::V8 V8;
+  constexpr int PARTS = M::kParts, U = DIM / 64, CB = DIM / 16, ROWS = 16 * NT;
+  extern __shared__ __align__(16) uint8_t lds[];
+
+  int64_t block = blockIdx.x;
+  const int split = (int)(block % A.splits);
+  block /= A.splits;
+  const int rt = (int)(block % A.row_tiles);
+  block /= A.row_tiles;
+  const int h = (int)(block % A.c.heads), b = (int)(block / A.c.heads);
+  const Sequence sq = sequence(A.s, b);
+  const int rows = sq.count * A.group, row0 = rt * ROWS;
+  if (row0 >= rows) return;
+  const int nrows = rows - row0 < ROWS ? rows - row0 : ROWS;
+  const Span sp = span_of(A, sq, row0 / A.group, (row0 + nrows - 1) / A.group);
+  const int64_t lo64 = (int64_t)sp.begin + (int64_t)split * A.chunk;
+  // a split behind the end writes nothing: the join counts the splits itself;
+  // the first one always writes, so that rows that see nothing become zeros
+  if (split > 0 && lo64 >= sp.end) return;
+  const int lo = (int)lo64;
+  const int hi = sp.end - lo < A.chunk ? sp.end : lo + A.chunk;
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+
+  // queries as operands: [NT][2 U steps][PARTS][64 lanes] of 16 bytes, the
+  // step (u, s) of lane (n, g) holding channels 64 u + 16 g + 8 s .. + 7
+  V8* ql = (V8*)lds;
+  for (int i = threadIdx.x; i < ROWS * (DIM / 8); i += 64 * kFewWaves) {
+    const int r = i / (DIM / 8), c8 = i % (DIM / 8);
+    float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (r < nrows) {
+      const int row = row0 + r, t = row / A.group, hh = h * A.group + row % A.group;
+      load_row8((const T*)A.q + (int64_t)(sq.row0 + t) * A.q_token + (int64_t)hh * A.q_head + 8 * c8, A.vec, x);
+    }
+    V8 p[PARTS];
+    to_parts<T>(x, p);
+    const int u = c8 / 8, gg = (c8 / 2) % 4, s = c8 % 2;
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) ql[(((r / 16) * 2 * U + 2 * u + s) * PARTS + k) * 64 + gg * 16 + r % 16] = p[k];
+  }
+  __syncthreads();
+
+  float m[NT], l[NT];
+  f32x4_t o[NT][CB];
+  int pos[NT];   // the column's position; -1: no row
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    m[nt] = -__builtin_inff();
+    l[nt] = 0.0f;
+    const int r = nt * 16 + n;
+    pos[nt] = r < nrows ? sp.first - row0 / A.group + (row0 + r) / A.group : -1;
+#pragma unroll
+    for (int c = 0; c < CB; ++c) o[nt][c] = f32x4_t{0, 0, 0, 0};
+  }
+
+  const int shift = A.c.page_shift, pmask = (1 << shift) - 1;
+  const int32_t* table = A.s.table + (int64_t)b * A.s.width;
+  const int64_t page_bytes = (int64_t)DIM << shift;
+
+  // the page of token t; -1 where it is not there
+  auto page_of = [&](int t) -> int {
+    if (t >= hi) return -1;
+    const int id = table[t >> shift];
+    return id < A.c.pages ? id : -1;
+  };
+
+  constexpr int STEP = 64 * kFewWaves;
+  uint4 kreg[4][U], vreg[CB];
+  int idv_next = -1;
+  float kscale = 0.0f, vexp = 0.0f;
+  int kbyte = 0, vbyte = 0;
+
+  // Key rows of lane n come from token group n / 4, values from group g.
+  auto load_k = [&](int t0, int id) {
+    const int64_t ph = (int64_t)(id < 0 ? 0 : id) * A.c.heads + h;
+    const uint8_t* p = A.c.k + ph * page_bytes + (int64_t)((t0 & pmask) + ((n >> 2) * 16 & pmask) + (n & 3)) * DIM + 16 * g;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int u = 0; u < U; ++u) kreg[t][u] = *(const uint4*)(p + 4 * t * DIM + 64 * u);
+  };
+  auto load_v = [&](int t0, int id) {
+    const int64_t ph = (int64_t)(id < 0 ? 0 : id) * A.c.heads + h;
+    const uint8_t* p = A.c.v + ph * page_bytes + ((int64_t)n << shift) + ((t0 & pmask) + (g * 16 & pmask));
+#pragma unroll
+    for (int c = 0; c < CB; ++c) vreg[c] = *(const uint4*)(p + ((int64_t)(16 * c) << shift));
+    kbyte = A.c.ks[ph];
+    vbyte = A.c.vs[ph];
+  };
+
+  int t0 = lo + wave * 64;
+  int idk = -1, idv = -1;
+  if (t0 < hi) {
+    idk = page_of(t0 + (n >> 2) * 16);
+    idv = page_of(t0 + g * 16);
+    load_k(t0, idk);
+    load_v(t0, idv);
+  }
+  for (; t0 < hi; t0 += STEP) {
+    const int t_next = t0 + STEP;
+    asm volatile("" ::: "memory");   // the query operands are read from LDS in each tile: held, they would fill the registers
+    const int idk_next = page_of(t_next + (n >> 2) * 16);
+    idv_next = page_of(t_next + g * 16);
+    kscale = __builtin_ldexpf(A.scale_log2, kbyte - 127);
+    vexp = (float)(vbyte - 127);
+
+    // S^T
+    f32x4_t sc[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) sc[nt][t] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        V8 a[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) a[t] = s ? decode8<V8>(kreg[t][u].z, kreg[t][u].w) : decode8<V8>(kreg[t][u].x, kreg[t][u].y);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < PARTS; ++k) {
+            const V8 bq = ql[((nt * 2 * U + 2 * u + s) * PARTS + k) * 64 + lane];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) sc[nt][t] = M::mul(a[t], bq, sc[nt][t]);
+          }
+      }
+    }
+    if (t_next < hi) load_k(t_next, idk_next);
+
+    // what each row sees; a tile that all rows see whole needs no comparison
+    const bool whole = t0 + 63 <= sp.first && (A.window <= 0 || t0 > sp.last - A.window) && t0 + 64 <= hi &&
+                       nrows == ROWS && __all(idv >= 0);
+    float e = vexp < -60.0f ? -60.0f : vexp > 60.0f ? 60.0f : vexp;
+    const float rest = pow2(vexp - e), back = pow2(-e);
+    V8 pw[NT][2][PARTS];
+    uint32_t seen[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      seen[nt] = 0xffffu;
+      if (!whole) {
+        seen[nt] = 0;
+        const int tg = t0 + 16 * g;
+        // tokens tg + i with i <= last_i and i >= first_i
+        const int last_i = (pos[nt] < hi ? pos[nt] : hi - 1) - tg;
+        const int first_i = A.window > 0 ? pos[nt] - A.window + 1 - tg : 0;
+        if (idv >= 0) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) seen[nt] |= (i <= last_i && i >= first_i) ? 1u << i : 0u;
+        }
+      }
+      float w[16], top = -__builtin_inff();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        w[i] = __builtin_fmaf(sc[nt][i / 4][i % 4], kscale, e);
+        if (!whole) w[i] = (seen[nt] >> i) & 1 ? w[i] : -__builtin_inff();
+        top = fmaxf(top, w[i]);
+      }
+      const float m_new = fmaxf(m[nt], max_across_groups(top));
+      const float base = m_new == -__builtin_inff() ? 0.0f : m_new;
+      const float alpha = pow2(m[nt] - base);
+      m[nt] = m_new;
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        w[i] = pow2(w[i] - base);
+        sum += w[i];
+      }
+      l[nt] = __builtin_fmaf(sum, back, l[nt] * alpha);
+#pragma unroll
+      for (int c = 0; c < CB; ++c) o[nt][c] *= alpha;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = w[8 * s + i] * rest;
+        to_parts<T>(x, pw[nt][s]);
+      }
+    }
+
+    // O^T
+    bool nan = false;
+    if (!whole) {
+      uint32_t any = 0;
+#pragma unroll
+      for (int c = 0; c < CB; ++c) any |= nan_bytes(vreg[c].x) | nan_bytes(vreg[c].y) | nan_bytes(vreg[c].z) | nan_bytes(vreg[c].w);
+      nan = __any(any != 0);
+    }
+    if (!nan) {
+#pragma unroll
+      for (int c = 0; c < CB; ++c) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const V8 a = s ? decode8<V8>(vreg[c].z, vreg[c].w) : decode8<V8>(vreg[c].x, vreg[c].y);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k) o[nt][c] = M::mul(a, pw[nt][s][k], o[nt][c]);
+        }
+      }
+    } else {
+      // NaN codes as zeros, and beside it the number of NaN codes that a row
+      // sees: where there is one, the row's channel is NaN
+#pragma unroll
+      for (int c = 0; c < CB; ++c) {
+        f32x4_t hits[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) hits[nt] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const uint32_t w0 = s ? vreg[c].z : vreg[c].x, w1 = s ? vreg[c].w : vreg[c].y;
+          const uint32_t n0 = nan_bytes(w0), n1 = nan_bytes(w1);
+          const V8 a = decode8<V8>(w0 & ~(n0 | (n0 - (n0 >> 7))), w1 & ~(n1 | (n1 - (n1 >> 7))));
+          const V8 ones = decode8<V8>(nan_ones(n0), nan_ones(n1));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k) o[nt][c] = M::mul(a, pw[nt][s][k], o[nt][c]);
+            V8 vis;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) vis[i] = (typename M::E)(float)((seen[nt] >> (8 * s + i)) & 1);
+            hits[nt] = M::mul(ones, vis, hits[nt]);
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[nt][c][i] = hits[nt][i] > 0.0f ? __builtin_nanf("") : o[nt][c][i];
+      }
+    }
+    if (t_next < hi) load_v(t_next, idv_next);
+    idk = idk_next;
+    idv = idv_next;
+  }
+
+  // join the waves: common maximum, then the sums of waves 2 and 3 through LDS
+  // to waves 0 and 1, and of wave 1 to wave 0
+  __syncthreads();
+  f32x4_t* red = (f32x4_t*)lds;                                 // [2][NT][CB][64]
+  float* ml = (float*)(lds + 2 * NT * CB * 64 * 16);            // [waves][NT][16][2]
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const float sum = sum_across_groups(l[nt]);
+    if (g == 0) {
+      ml[((wave * NT + nt) * 16 + n) * 2] = m[nt];
+      ml[((wave * NT + nt) * 16 + n) * 2 + 1] = sum;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float top = -__builtin_inff(), sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w) top = fmaxf(top, ml[((w * NT + nt) * 16 + n) * 2]);
+    const float base = top == -__builtin_inff() ? 0.0f : top;
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w)
+      sum += ml[((w * NT + nt) * 16 + n) * 2 + 1] * pow2(ml[((w * NT + nt) * 16 + n) * 2] - base);
+    const float f = pow2(m[nt] - base);
+#pragma unroll
+    for (int c = 0; c < CB; ++c) o[nt][c] *= f;
+    m[nt] = top;
+    l[nt] = sum;
+  }
+#pragma unroll
+  for (int half = kFewWaves / 2; half >= 1; half /= 2) {
+    if (wave >= half && wave < 2 * half) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < CB; ++c) red[(((wave - half) * NT + nt) * CB + c) * 64 + lane] = o[nt][c];
+    }
+    __syncthreads();
+    if (wave < half) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < CB; ++c) o[nt][c] += red[((wave * NT + nt) * CB + c) * 64 + lane];
+    }
+    __syncthreads();
+  }
+  if (wave != 0) return;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = nt * 16 + n;
+    if (r >= nrows) continue;
+    const int row = row0 + r, t = row / A.group, hh = h * A.group + row % A.group;
+    const int64_t at = (int64_t)(sq.row0 + t) * A.heads_q + hh;
+    if (A.splits == 1) {
+      T* out = (T*)A.out + at * DIM;
+#pragma unroll
+      for (int c = 0; c < CB; ++c) {
+        typedef T vec4 __attribute__((ext_vector_type(4)));
+        vec4 y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = (T)(l[nt] == 0.0f ? 0.0f : o[nt][c][i] / l[nt]);
+        *(vec4*)(out + 16 * c + 4 * g) = y;
+      }
+    } else {
+      const int64_t ps = at * A.splits + split;
+      if (g == 0) {
+        A.part_m[ps] = m[nt];
+        A.part_l[ps] = l[nt];
+      }
+      float* po = A.part_o + ps * DIM;
+#pragma unroll
+      for (int c = 0; c < CB; ++c) *(f32x4_t*)(po + 16 * c + 4 * g) = o[nt][c];
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Join of a split axis: a block per output row
+// ---------------------------------------------------------------------------
+template <typename T, int DIM>
+__global__ __launch_bounds__(256) void join_kernel(AttnArgs A, int rows_per_tile) {
+  __shared__ float sum_o[4][DIM];
+  __shared__ float sum_l[4];
+  const int64_t at = blockIdx.x;
+  const int t_abs = (int)(at / A.heads_q), hh = (int)(at % A.heads_q);
+  int b = t_abs;
+  if (A.s.cu) {
+    int lo = 0, hi = A.s.batch;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (A.s.cu[mid + 1] <= t_abs) lo = mid + 1; else hi = mid;
+    }
+    b = lo;
+  }
+  if (b >= A.s.batch) return;
+  const Sequence sq = sequence(A.s, b);
+  const int t = t_abs - sq.row0;
+  if (t < 0 || t >= sq.count) return;
+  const int row = t * A.group + hh % A.group, rows = sq.count * A.group, row0 = row / rows_per_tile * rows_per_tile;
+  const int last = (row0 + rows_per_tile < rows ? row0 + rows_per_tile : rows) - 1;
+  const Span sp = span_of(A, sq, row0 / A.group, last / A.group);
+  int n = sp.end > sp.begin ? (sp.end - sp.begin + A.chunk - 1) / A.chunk : 1;
+  n = n < A.splits ? n : A.splits;
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const float* pm = A.part_m + at * A.splits;
+  const float* pl = A.part_l + at * A.splits;
+  float mx = -__builtin_inff();
+  for (int i = lane; i < n; i += 64) mx = fmaxf(mx, pm[i]);
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off, 64));
+  const float base = mx == -__builtin_inff() ? 0.0f : mx;
+  float acc[DIM / 64], l = 0.0f;
+#pragma unroll
+  for (int c = 0; c < DIM / 64; ++c) acc[c] = 0.0f;
+  for (int i = wave; i < n; i += 4) {
+    const float f = pow2(pm[i] - base);
+    l = __builtin_fmaf(pl[i], f, l);
+    const float* po = A.part_o + (at * A.splits + i) * DIM;
+#pragma unroll
+    for (int c = 0; c < DIM / 64; ++c) acc[c] = __builtin_fmaf(po[c * 64 + lane], f, acc[c]);
+  }
+#pragma unroll
+  for (int c = 0; c < DIM / 64; ++c) sum_o[wave][c * 64 + lane] = acc[c];
+  if (lane == 0) sum_l[wave] = l;
+  __syncthreads();
+  l = (sum_l[0] + sum_l[1]) + (sum_l[2] + sum_l[3]);
+  for (int c = threadIdx.x; c < DIM; c += 256) {
+    const float o = (sum_o[0][c] + sum_o[1][c]) + (sum_o[2][c] + sum_o[3][c]);
+    store_out((T*)A.out + at * DIM + c, l == 0.0f ? 0.0f : o / l);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// plan
+// ---------------------------------------------------------------------------
+
+struct Plan {
+  int nt;             // columns / 16 of the few-rows kernel
+  int rows;           // rows of a tile
+  int64_t row_tiles;  // of a sequence and head, at most
+  int64_t splits, chunk, blocks;
+};
+
+Plan make_plan(int64_t heads_q, int64_t heads, int64_t page, int64_t batch, int64_t max_q,
+               int64_t width, int64_t window, bool split) {
+  Plan p;
+  const int64_t group = heads_q / heads, rows = max_q * group;
+  p.nt = rows <= 16 ? 1 : 2;
+  p.rows = 16 * p.nt;
+  p.row_tiles = (rows + p.rows - 1) / p.rows;
+  // the longest span of a tile of rows, from a tile boundary on
+  int64_t span = width * page;
+  if (window > 0) {
+    const int64_t w = window - 1 + (p.rows + group - 1) / group + 1 + 63;
+    if (w < span) span = w;
+  }
+  const int64_t tiles = (span + 63) / 64, base = batch * heads * p.row_tiles;
+  p.splits = 1;
+  p.chunk = (tiles > 0 ? tiles : 1) * 64;
+  if (split) {
+    // enough blocks for three rounds on the chip, and four tiles a wave at least
+    int64_t want = (3 * 512 + base - 1) / base;
+    const int64_t most = (tiles + 15) / 16;
+    if (want > most) want = most;
+    if (want > 1) {
+      p.chunk = ((tiles + want - 1) / want + kFewWaves - 1) / kFewWaves * kFewWaves * 64;
+      p.splits = (tiles * 64 + p.chunk - 1) / p.chunk;
+    }
+  }
+  p.blocks = base * p.splits;
+  return p;
+}
+
+int64_t partials(const Plan& p, int64_t tokens, int64_t heads_q, int64_t dim) {
+  return p.splits > 1 ? tokens * heads_q * p.splits * (dim + 2) * 4 : 0;
+}
+
+template <typename T, int DIM, int NT>
+bool launch_few(const AttnArgs& A, int64_t blocks, hipStream_t s) {
+  constexpr int bytes = few_lds_bytes<DIM, NT, Mma<T>::kParts>();
+  static_assert(bytes <= 160 * 1024, "LDS of a workgroup");
+  if constexpr (bytes > 64 * 1024) {
+    if (hipFuncSetAttribute((const void*)few_rows_kernel<T, DIM, NT>, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
+      return false;
+  }
+  few_rows_kernel<T, DIM, NT><<<dim3((uint32_t)blocks), dim3(64 * kFewWaves), bytes, s>>>(A);
+  return true;
+}
+
+template <typename T, int DIM>
+void launch_dim(const AttnArgs& A, const Plan& p, hipStream_t s) {
+  const bool ok = p.nt == 1 ? launch_few<T, DIM, 1>(A, p.blocks, s) : launch_few<T, DIM, 2>(A, p.blocks, s);
+  if (ok && p.splits > 1)
+    join_kernel<T, DIM><<<dim3((uint32_t)((int64_t)A.s.tokens * A.heads_q)), dim3(256), 0, s>>>(A, p.rows);
+}
+
+template <typename T>
+void launch_type(const AttnArgs& A, const Plan& p, int64_t dim, hipStream_t s) {
+  switch (dim) {
+    case 64: launch_dim<T, 64>(A, p, s); break;
+    case 128: launch_dim<T, 128>(A, p, s); break;
+    case 192: launch_dim<T, 192>(A, p, s); break;
+    case 256: launch_dim<T, 256>(A, p, s); break;
+  }
+}
+
+}  // namespace
+
+namespace nvfp4host {
+
+int64_t paged_attention_bytes(int64_t tokens, int64_t heads_q, int64_t heads, int64_t dim, int64_t page, int64_t batch,
+                              int64_t max_q, int64_t width, int64_t window, nvfp4_dtype_t) {
+  return (partials(make_plan(heads_q, heads, page, batch, max_q, width, window, true), tokens, heads_q, dim) + 255) / 256 * 256;
+}
+
+int64_t paged_attention_blocks(int64_t heads_q, int64_t heads, int64_t page, int64_t batch, int64_t max_q, int64_t width,
+                               int64_t window) {
+  return make_plan(heads_q, heads, page, batch, max_q, width, window, true).blocks;
+}
+
+void launch_paged_attention(const nvfp4_kv_cache_t& c, const void* q, int64_t q_token, int64_t q_head, int64_t heads_q,
+                            nvfp4_dtype_t dt, int64_t tokens, const int32_t* cu, int64_t batch, int64_t max_q,
+                            const int32_t* table, int64_t width, const int32_t* lens, int64_t window, float scale,
+                            void* ws, int64_t ws_bytes, void* out, hipStream_t s) {
+  Plan p = make_plan(heads_q, c.heads, c.page, batch, max_q, width, window, true);
+  if (ws_bytes < partials(p, tokens, heads_q, c.dim)) p = make_plan(heads_q, c.heads, c.page, batch, max_q, width, window, false);
+  AttnArgs A;
+  A.c = {c.k, c.v, c.k_scales, c.v_scales, (int32_t)c.pages, (int32_t)c.heads, __builtin_ctz((unsigned)c.page)};
+  A.s = {table, lens, cu, width, (int32_t)batch, (int32_t)tokens};
+  A.q = q; A.q_token = q_token; A.q_head = q_head;
+  A.out = out;
+  if (c.pages == 0) A.s.width = 0;   // no page to read: nothing is seen
+  const int64_t prow = tokens * heads_q * p.splits;
+  A.part_o = (float*)ws;
+  A.part_m = p.splits > 1 ? A.part_o + prow * c.dim : nullptr;
+  A.part_l = p.splits > 1 ? A.part_m + prow : nullptr;
+  A.heads_q = (int32_t)heads_q; A.group = (int32_t)(heads_q / c.heads);
+  A.window = window >= width * c.page ? 0 : (int32_t)window;   // a window over the whole table is none
+  A.splits = (int32_t)p.splits; A.chunk = (int32_t)p.chunk;
+  A.row_tiles = (int32_t)p.row_tiles;
+  A.scale_log2 = scale * kLog2e;
+  const int64_t size = dt == NVFP4_F32 ? 4 : 2;
+  A.vec = ((uintptr_t)q & 15) == 0 && (q_token * size) % 16 == 0 && (q_head * size) % 16 == 0;
+  switch (dt) {
+    case NVFP4_F32: launch_type<float>(A, p, c.dim, s); break;
+    case NVFP4_BF16: launch_type<__bf16>(A, p, c.dim, s); break;
+    case NVFP4_F16: launch_type<_Float16>(A, p, c.dim, s); break;
+  }
+}
+
+}  // namespace nvfp4host

@@ -126,6 +126,31 @@ void launch_gather(const void* x, nvfp4_dtype_t dt, int64_t X, int64_t M, int64_
                    const uint8_t* sc, const float* gs, int64_t E, int64_t N, int sorted,
                    void* out, hipStream_t s);
 
+// Appends new tokens to the paged 8-bit cache and rotates queries (heads_q 0:
+// none); kv_append_blocks is an upper bound of its grid.
+int64_t kv_append_blocks(int64_t page, int64_t heads, int64_t heads_q, int64_t tokens, int64_t batch, int64_t max_q);
+void launch_kv_append(const nvfp4_kv_cache_t& c, const void* k, int64_t k_token, int64_t k_head, const void* v,
+                      int64_t v_token, int64_t v_head, const void* q, int64_t q_token, int64_t q_head,
+                      int64_t heads_q, void* q_out, nvfp4_dtype_t dt, int64_t tokens, const int32_t* cu,
+                      int64_t batch, int64_t max_q, const int32_t* table, int64_t width, const int32_t* lens,
+                      const float* inv_freq, int64_t rot, bool inter, hipStream_t s);
+// Attention over the paged cache.  paged_attention_bytes is the workspace that
+// a split of the token axis wants (0: none), paged_attention_blocks its grid.
+int64_t paged_attention_bytes(int64_t tokens, int64_t heads_q, int64_t heads, int64_t dim, int64_t page, int64_t batch,
+                              int64_t max_q, int64_t width, int64_t window, nvfp4_dtype_t dt);
+int64_t paged_attention_blocks(int64_t heads_q, int64_t heads, int64_t page, int64_t batch, int64_t max_q, int64_t width,
+                               int64_t window);
+void launch_paged_attention(const nvfp4_kv_cache_t& c, const void* q, int64_t q_token, int64_t q_head, int64_t heads_q,
+                            nvfp4_dtype_t dt, int64_t tokens, const int32_t* cu, int64_t batch, int64_t max_q,
+                            const int32_t* table, int64_t width, const int32_t* lens, int64_t window, float scale,
+                            void* ws, int64_t ws_bytes, void* out, hipStream_t s);
+// One token per row of logits; sample_bytes is the workspace with which
+// several blocks share a row (0: none).
+int64_t sample_bytes(int64_t batch, int64_t vocab, nvfp4_dtype_t dt);
+void launch_sample(const void* logits, nvfp4_dtype_t dt, int64_t batch, int64_t vocab, int64_t row_stride, const float* u,
+                   const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p, void* ws,
+                   int64_t ws_bytes, int32_t* token, float* prob, hipStream_t s);
+
 // Grid limits used by the launchers (HIP: gridDim.x < 2^31, y/z < 2^16).
 constexpr int64_t kMaxGridX = 2147483647LL;
 constexpr int64_t kMaxGridY = 65535;
