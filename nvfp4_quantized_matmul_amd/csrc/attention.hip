@@ -508,6 +508,345 @@ __global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>:
 }
 
 // ---------------------------------------------------------------------------
+// Many rows: the waves of a block share the tokens and split the rows
+// ---------------------------------------------------------------------------
+//
+// 2-byte types.  Each of four waves has 32 rows; a tile of 64 tokens is
+// converted once for all of them on its way into LDS, where two tiles
+// alternate: while one is multiplied the next one's codes are on their way to
+// registers, and one barrier a tile is enough.  The 32x32 multiply reads each
+// LDS operand for twice as many rows as the 16x16 one; at 32 rows a wave the
+// LDS and the matrix cores are then about equally busy.
+//
+// Lane (n, hh) = (lane % 32, lane / 32) holds of multiply tt tokens 32 tt + 16
+// s + 8 hh + (0..7) of column n, s = 0, 1: an operand of the second product
+// per s.  Key rows therefore lie in LDS in the order in which the result has
+// them.  Rows of LDS are stored with their 16-byte pieces permuted by the row
+// number, so that lanes reading down a column of pieces meet all banks.
+//
+// The running maximum is raised only once a score passes it by 2^8: a weight
+// of 256 is as exact in every type as one of 1, and most tiles leave the sums
+// alone.
+constexpr int kManyWaves = 4, kManyRows = 32 * kManyWaves;
+
+template <typename T>
+struct Mma32;
+template <>
+struct Mma32<__bf16> {
+  static __device__ __forceinline__ f32x16_t mul(bf16x8_t a, bf16x8_t b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+};
+template <>
+struct Mma32<_Float16> {
+  static __device__ __forceinline__ f32x16_t mul(f16x8_t a, f16x8_t b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  }
+};
+
+// What the four groups of 16 tokens of a tile have in common.
+struct GroupInfo {
+  float kscale, e, rest, back;   // score factor; clamped exponent of the values, what the clamp left, 2^-e
+};
+
+template <int DIM>
+struct ManyTile {
+  uint4 k[64 * DIM / 8];   // [64 rows][DIM / 8] pieces of 8 elements
+  uint4 v[DIM * 8];        // [DIM channels][8]
+};
+
+template <int DIM>
+struct ManyShared {
+  ManyTile<DIM> tile[2];
+  GroupInfo info[2][4];
+  uint32_t there[2];   // bit g: group g's page is there
+  int32_t nan[2];      // the first token of the last partial tile here that had a NaN code among its values,
+  __align__(8) uint16_t nan_tokens[2][DIM][4];   // and which ones: a bit per token
+};
+
+template <typename T, int DIM>
+__global__ __launch_bounds__(64 * kManyWaves, DIM <= 128 ? 2 : 1) void many_rows_kernel(AttnArgs A) {
+  typedef typename Mma<T>::V8 V8;
+  typedef typename Mma<T>::E E;
+  constexpr int KS = DIM / 16, CB = DIM / 32, KP = DIM / 8, THREADS = 64 * kManyWaves;
+  constexpr int KLOADS = 64 * DIM / 16 / THREADS;   // 16-byte loads of a thread and tile, of keys and of values
+  static_assert(KLOADS * THREADS * 16 == 64 * DIM, "whole rounds");
+  extern __shared__ __align__(16) uint8_t lds[];
+  ManyShared<DIM>& S = *(ManyShared<DIM>*)lds;
+
+  // the longest row tiles first; splits, heads and sequences side by side
+  int64_t block = blockIdx.x;
+  const int split = (int)(block % A.splits);
+  block /= A.splits;
+  const int h = (int)(block % A.c.heads);
+  block /= A.c.heads;
+  const int b = (int)(block % A.s.batch);
+  const int rt = A.row_tiles - 1 - (int)(block / A.s.batch);
+  const Sequence sq = sequence(A.s, b);
+  const int rows = sq.count * A.group, row0 = rt * kManyRows;
+  if (row0 >= rows) return;
+  const int nrows = rows - row0 < kManyRows ? rows - row0 : kManyRows;
+  const Span sp = span_of(A, sq, row0 / A.group, (row0 + nrows - 1) / A.group);
+  const int64_t lo64 = (int64_t)sp.begin + (int64_t)split * A.chunk;
+  if (split > 0 && lo64 >= sp.end) return;
+  const int lo = (int)lo64;
+  const int hi = sp.end - lo < A.chunk ? sp.end : lo + A.chunk;
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 31, hh = lane >> 5;
+  const int shift = A.c.page_shift, pmask = (1 << shift) - 1;
+  const int32_t* table = A.s.table + (int64_t)b * A.s.width;
+  const int64_t page_bytes = (int64_t)DIM << shift;
+
+  // the wave's queries, in registers: step s holds channels 16 s + 8 hh .. + 7
+  const int my = wave * 32 + n, base_pos = sq.len - sq.count;
+  const int pos = my < nrows ? base_pos + (row0 + my) / A.group : -1;
+  V8 q[KS];
+  {
+    const int row = row0 + (my < nrows ? my : 0), t = row / A.group, head = h * A.group + row % A.group;
+    const T* p = (const T*)A.q + (int64_t)(sq.row0 + t) * A.q_token + (int64_t)head * A.q_head + 8 * hh;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      float x[8];
+      load_row8(p + 16 * s, A.vec, x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[s][i] = (E)(my < nrows ? x[i] : 0.0f);
+    }
+  }
+  // positions of the wave's first and last row: rows are in the order of positions
+  const int wave_rows = nrows - wave * 32 < 32 ? nrows - wave * 32 : 32;
+  const int wfirst = wave_rows > 0 ? base_pos + (row0 + wave * 32) / A.group : 0;
+  const int wlast = wave_rows > 0 ? base_pos + (row0 + wave * 32 + wave_rows - 1) / A.group : -1;
+
+  auto page_of = [&](int t) -> int {
+    if (t >= hi) return -1;
+    const int id = table[t >> shift];
+    return id < A.c.pages ? id : -1;
+  };
+  // a thread's loads: piece i THREADS + tid of the keys, DIM / 16 of them a
+  // row; values of channel tid / 4 + i THREADS / 4, tokens 16 (tid % 4)
+  const int vch = tid / 4, vg = tid % 4;
+  int krow[KLOADS], kc[KLOADS];
+#pragma unroll
+  for (int i = 0; i < KLOADS; ++i) {
+    krow[i] = (i * THREADS + tid) / (DIM / 16);
+    kc[i] = (i * THREADS + tid) % (DIM / 16);
+  }
+  uint4 kreg[KLOADS], vreg[KLOADS];
+  int idk[KLOADS], idv;
+  int kbyte = 0, vbyte = 0;
+  auto ids = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < KLOADS; ++i) idk[i] = page_of(t0 + krow[i]);
+    idv = page_of(t0 + 16 * vg);
+  };
+  auto load = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < KLOADS; ++i) {
+      const int64_t ph = (int64_t)(idk[i] < 0 ? 0 : idk[i]) * A.c.heads + h;
+      kreg[i] = *(const uint4*)(A.c.k + ph * page_bytes + (int64_t)((t0 + krow[i]) & pmask) * DIM + 16 * kc[i]);
+    }
+    const int64_t ph = (int64_t)(idv < 0 ? 0 : idv) * A.c.heads + h;
+    const uint8_t* p = A.c.v + ph * page_bytes + ((int64_t)vch << shift) + ((t0 + 16 * vg) & pmask);
+#pragma unroll
+    for (int i = 0; i < KLOADS; ++i) vreg[i] = *(const uint4*)(p + ((int64_t)(i * (THREADS / 4)) << shift));
+    kbyte = A.c.ks[ph];
+    vbyte = A.c.vs[ph];
+  };
+  // converts the loaded tile into LDS; `part`: some row of the block does not see all of it
+  auto store = [&](int at, int t0, bool part) {
+    ManyTile<DIM>& t = S.tile[at];
+    if (part) {
+      uint32_t any = 0;
+#pragma unroll
+      for (int i = 0; i < KLOADS; ++i) {
+        uint32_t* w = &vreg[i].x;
+        uint32_t bits = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t nan = nan_bytes(w[k]);
+          w[k] &= ~(nan | (nan - (nan >> 7)));
+          bits |= (((nan >> 7) * 0x10204080u) >> 28) << (4 * k);   // bits 7, 15, 23, 31 side by side
+        }
+        S.nan_tokens[at][vch + i * (THREADS / 4)][vg] = (uint16_t)bits;
+        any |= bits;
+      }
+      if (__any(any != 0) && lane == 0) S.nan[at] = t0;
+    }
+#pragma unroll
+    for (int i = 0; i < KLOADS; ++i) {
+      const int tok = krow[i];
+      const int r = (tok & 32) | (tok & 16) | ((tok & 4) << 1) | ((tok & 8) >> 1) | (tok & 3);
+      t.k[r * KP + ((2 * kc[i]) ^ (r & 7))] = __builtin_bit_cast(uint4, decode8<V8>(kreg[i].x, kreg[i].y));
+      t.k[r * KP + ((2 * kc[i] + 1) ^ (r & 7))] = __builtin_bit_cast(uint4, decode8<V8>(kreg[i].z, kreg[i].w));
+      const int c = vch + i * (THREADS / 4);
+      t.v[c * 8 + ((2 * vg) ^ (c & 7))] = __builtin_bit_cast(uint4, decode8<V8>(vreg[i].x, vreg[i].y));
+      t.v[c * 8 + ((2 * vg + 1) ^ (c & 7))] = __builtin_bit_cast(uint4, decode8<V8>(vreg[i].z, vreg[i].w));
+    }
+    if (tid < 4) {
+      GroupInfo f;
+      const float e = (float)(vbyte - 127);
+      f.kscale = __builtin_ldexpf(A.scale_log2, kbyte - 127);
+      f.e = e < -60.0f ? -60.0f : e > 60.0f ? 60.0f : e;
+      f.rest = pow2(e - f.e);
+      f.back = pow2(-f.e);
+      S.info[at][tid] = f;
+    }
+    if (wave == 0) {
+      const uint64_t there = __ballot(idv >= 0);
+      if (tid == 0) S.there[at] = (uint32_t)there & 0xfu;
+    }
+  };
+
+  f32x16_t o[CB];
+#pragma unroll
+  for (int c = 0; c < CB; ++c)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[c][i] = 0.0f;
+  float m = -__builtin_inff(), l = 0.0f;
+
+  // a tile is partial for the block if a row does not see it whole or a page is missing
+  auto partial = [&](int t0) -> bool {
+    return t0 + 63 > sp.first || (A.window > 0 && t0 <= sp.last - A.window) || t0 + 64 > hi || __any(idv < 0);
+  };
+
+  if (tid < 2) S.nan[tid] = -1;
+  __syncthreads();
+  int at = 0;
+  if (lo < hi) {
+    ids(lo);
+    load(lo);
+    store(0, lo, partial(lo));
+    ids(lo + 64);
+  }
+  for (int t0 = lo; t0 < hi; t0 += 64, at ^= 1) {
+    __syncthreads();
+    const bool more = t0 + 64 < hi;
+    bool next_partial = false;
+    if (more) {
+      load(t0 + 64);
+      next_partial = partial(t0 + 64);
+    }
+    const ManyTile<DIM>& t = S.tile[at];
+    const bool unseen = t0 > wlast || (A.window > 0 && t0 + 63 <= wfirst - A.window);
+    if (!unseen) {
+      f32x16_t sc[2];
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sc[tt][i] = 0.0f;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+          const int r = 32 * tt + n;
+          sc[tt] = Mma32<T>::mul(__builtin_bit_cast(V8, t.k[r * KP + ((2 * s + hh) ^ (r & 7))]), q[s], sc[tt]);
+        }
+      }
+      const uint32_t there = S.there[at];
+      const bool whole = t0 + 63 <= wfirst && (A.window <= 0 || t0 > wlast - A.window) && wave_rows == 32 && there == 0xfu;
+      float top = -__builtin_inff();
+      uint64_t vis = ~0ull;   // the tile's tokens that the lane's row sees
+      if (!whole) {
+        const int last_i = pos - t0, first_i = A.window > 0 ? pos - A.window + 1 - t0 : 0;
+        vis = last_i < 0 ? 0 : last_i >= 63 ? ~0ull : (2ull << last_i) - 1;
+        if (first_i > 0) vis = first_i > 63 ? 0 : vis & (~0ull << first_i);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) vis &= (there >> g) & 1 ? ~0ull : ~(0xffffull << (16 * g));
+      }
+      const uint32_t seen[2] = {(uint32_t)vis >> (8 * hh), (uint32_t)(vis >> 32) >> (8 * hh)};
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const float ck = S.info[at][2 * tt + s].kscale, e = S.info[at][2 * tt + s].e;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float x = __builtin_fmaf(sc[tt][8 * s + j], ck, e);
+            if (!whole) x = (seen[tt] >> (16 * s + j)) & 1 ? x : -__builtin_inff();
+            sc[tt][8 * s + j] = x;
+            top = fmaxf(top, x);
+          }
+        }
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      if (__any(top > m + 8.0f)) {
+        const float m_new = fmaxf(m, top);
+        const float alpha = pow2(m - (m_new == -__builtin_inff() ? 0.0f : m_new));
+        m = m_new;
+        l *= alpha;
+#pragma unroll
+        for (int c = 0; c < CB; ++c) o[c] *= alpha;
+      }
+      const float base = m == -__builtin_inff() ? 0.0f : m;
+      V8 pw[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const float back = S.info[at][g].back, rest = S.info[at][g].rest;
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float w = pow2(sc[g / 2][8 * (g % 2) + j] - base);
+          sum += w;
+          pw[g][j] = (E)(w * rest);
+        }
+        l = __builtin_fmaf(sum, back, l);
+      }
+#pragma unroll
+      for (int c = 0; c < CB; ++c) {
+        const int ch = 32 * c + n;
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          o[c] = Mma32<T>::mul(__builtin_bit_cast(V8, t.v[ch * 8 + ((2 * g + hh) ^ (ch & 7))]), pw[g], o[c]);
+      }
+      if (S.nan[at] == t0) {
+        // NaN codes lie as zeros in the tile: a channel with one that the row sees is NaN
+#pragma unroll
+        for (int c = 0; c < CB; ++c)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint64_t bad = *(const uint64_t*)S.nan_tokens[at][32 * c + 8 * (i / 4) + 4 * hh + i % 4];
+            o[c][i] = (bad & vis) ? __builtin_nanf("") : o[c][i];
+          }
+      }
+    }
+    if (more) {
+      store(at ^ 1, t0 + 64, next_partial);   // its readers have passed this round's barrier
+      ids(t0 + 128);
+    }
+  }
+
+  l += __shfl_xor(l, 32, 64);
+  if (my >= nrows) return;
+  const int row = row0 + my, tq = row / A.group, head = h * A.group + row % A.group;
+  const int64_t out_row = (int64_t)(sq.row0 + tq) * A.heads_q + head;
+  if (A.splits == 1) {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    T* out = (T*)A.out + out_row * DIM;
+#pragma unroll
+    for (int c = 0; c < CB; ++c)
+#pragma unroll
+      for (int i4 = 0; i4 < 4; ++i4) {
+        typedef T vec4 __attribute__((ext_vector_type(4)));
+        vec4 y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = (T)(l == 0.0f ? 0.0f : o[c][4 * i4 + i] * inv);
+        *(vec4*)(out + 32 * c + 8 * i4 + 4 * hh) = y;
+      }
+  } else {
+    const int64_t ps = out_row * A.splits + split;
+    if (hh == 0) {
+      A.part_m[ps] = m;
+      A.part_l[ps] = l;
+    }
+    float* po = A.part_o + ps * DIM;
+#pragma unroll
+    for (int c = 0; c < CB; ++c)
+#pragma unroll
+      for (int i4 = 0; i4 < 4; ++i4)
+        *(f32x4_t*)(po + 32 * c + 8 * i4 + 4 * hh) = f32x4_t{o[c][4 * i4], o[c][4 * i4 + 1], o[c][4 * i4 + 2], o[c][4 * i4 + 3]};
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Join of a split axis: a block per output row
 // ---------------------------------------------------------------------------
 template <typename T, int DIM>
@@ -569,22 +908,24 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs A, int rows_per_tile
 // ---------------------------------------------------------------------------
 
 struct Plan {
+  bool many;          // the many-rows kernel
   int nt;             // columns / 16 of the few-rows kernel
   int rows;           // rows of a tile
   int64_t row_tiles;  // of a sequence and head, at most
   int64_t splits, chunk, blocks;
 };
 
-Plan make_plan(int64_t heads_q, int64_t heads, int64_t page, int64_t batch, int64_t max_q,
-               int64_t width, int64_t window, bool split) {
+Plan make_plan(int64_t heads_q, int64_t heads, int64_t page, int64_t batch, int64_t max_q, int64_t width,
+               int64_t window, nvfp4_dtype_t dt, bool split) {
   Plan p;
   const int64_t group = heads_q / heads, rows = max_q * group;
+  p.many = dt != NVFP4_F32 && rows > 32;
   p.nt = rows <= 16 ? 1 : 2;
-  p.rows = 16 * p.nt;
+  p.rows = p.many ? kManyRows : 16 * p.nt;
   p.row_tiles = (rows + p.rows - 1) / p.rows;
   // the longest span of a tile of rows, from a tile boundary on
   int64_t span = width * page;
-  if (window > 0) {
+  if (window > 0 && window < span) {
     const int64_t w = window - 1 + (p.rows + group - 1) / group + 1 + 63;
     if (w < span) span = w;
   }
@@ -592,12 +933,14 @@ Plan make_plan(int64_t heads_q, int64_t heads, int64_t page, int64_t batch, int6
   p.splits = 1;
   p.chunk = (tiles > 0 ? tiles : 1) * 64;
   if (split) {
-    // enough blocks for three rounds on the chip, and four tiles a wave at least
-    int64_t want = (3 * 512 + base - 1) / base;
-    const int64_t most = (tiles + 15) / 16;
+    // few rows: three rounds of blocks on the chip, and four tiles a wave at
+    // least; many rows: one round, and eight tiles a block
+    const int64_t unit = p.many ? 1 : kFewWaves, least = p.many ? 8 : 4 * kFewWaves, full = p.many ? 512 : 3 * 512;
+    int64_t want = p.many ? full / base : (full + base - 1) / base;
+    const int64_t most = (tiles + least - 1) / least;
     if (want > most) want = most;
     if (want > 1) {
-      p.chunk = ((tiles + want - 1) / want + kFewWaves - 1) / kFewWaves * kFewWaves * 64;
+      p.chunk = ((tiles + want - 1) / want + unit - 1) / unit * unit * 64;
       p.splits = (tiles * 64 + p.chunk - 1) / p.chunk;
     }
   }
@@ -622,8 +965,22 @@ bool launch_few(const AttnArgs& A, int64_t blocks, hipStream_t s) {
 }
 
 template <typename T, int DIM>
+bool launch_many(const AttnArgs& A, int64_t blocks, hipStream_t s) {
+  constexpr int bytes = (int)sizeof(ManyShared<DIM>);
+  static_assert(bytes <= 160 * 1024, "LDS of a workgroup");
+  if (bytes > 64 * 1024 &&
+      hipFuncSetAttribute((const void*)many_rows_kernel<T, DIM>, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
+    return false;
+  many_rows_kernel<T, DIM><<<dim3((uint32_t)blocks), dim3(64 * kManyWaves), bytes, s>>>(A);
+  return true;
+}
+
+template <typename T, int DIM>
 void launch_dim(const AttnArgs& A, const Plan& p, hipStream_t s) {
-  const bool ok = p.nt == 1 ? launch_few<T, DIM, 1>(A, p.blocks, s) : launch_few<T, DIM, 2>(A, p.blocks, s);
+  bool ok = false;
+  if constexpr (sizeof(T) == 2)
+    if (p.many) ok = launch_many<T, DIM>(A, p.blocks, s);
+  if (!p.many) ok = p.nt == 1 ? launch_few<T, DIM, 1>(A, p.blocks, s) : launch_few<T, DIM, 2>(A, p.blocks, s);
   if (ok && p.splits > 1)
     join_kernel<T, DIM><<<dim3((uint32_t)((int64_t)A.s.tokens * A.heads_q)), dim3(256), 0, s>>>(A, p.rows);
 }
@@ -643,21 +1000,21 @@ void launch_type(const AttnArgs& A, const Plan& p, int64_t dim, hipStream_t s) {
 namespace nvfp4host {
 
 int64_t paged_attention_bytes(int64_t tokens, int64_t heads_q, int64_t heads, int64_t dim, int64_t page, int64_t batch,
-                              int64_t max_q, int64_t width, int64_t window, nvfp4_dtype_t) {
-  return (partials(make_plan(heads_q, heads, page, batch, max_q, width, window, true), tokens, heads_q, dim) + 255) / 256 * 256;
+                              int64_t max_q, int64_t width, int64_t window, nvfp4_dtype_t dt) {
+  return (partials(make_plan(heads_q, heads, page, batch, max_q, width, window, dt, true), tokens, heads_q, dim) + 255) / 256 * 256;
 }
 
 int64_t paged_attention_blocks(int64_t heads_q, int64_t heads, int64_t page, int64_t batch, int64_t max_q, int64_t width,
-                               int64_t window) {
-  return make_plan(heads_q, heads, page, batch, max_q, width, window, true).blocks;
+                               int64_t window, nvfp4_dtype_t dt) {
+  return make_plan(heads_q, heads, page, batch, max_q, width, window, dt, true).blocks;
 }
 
 void launch_paged_attention(const nvfp4_kv_cache_t& c, const void* q, int64_t q_token, int64_t q_head, int64_t heads_q,
                             nvfp4_dtype_t dt, int64_t tokens, const int32_t* cu, int64_t batch, int64_t max_q,
                             const int32_t* table, int64_t width, const int32_t* lens, int64_t window, float scale,
                             void* ws, int64_t ws_bytes, void* out, hipStream_t s) {
-  Plan p = make_plan(heads_q, c.heads, c.page, batch, max_q, width, window, true);
-  if (ws_bytes < partials(p, tokens, heads_q, c.dim)) p = make_plan(heads_q, c.heads, c.page, batch, max_q, width, window, false);
+  Plan p = make_plan(heads_q, c.heads, c.page, batch, max_q, width, window, dt, true);
+  if (ws_bytes < partials(p, tokens, heads_q, c.dim)) p = make_plan(heads_q, c.heads, c.page, batch, max_q, width, window, dt, false);
   AttnArgs A;
   A.c = {c.k, c.v, c.k_scales, c.v_scales, (int32_t)c.pages, (int32_t)c.heads, __builtin_ctz((unsigned)c.page)};
   A.s = {table, lens, cu, width, (int32_t)batch, (int32_t)tokens};

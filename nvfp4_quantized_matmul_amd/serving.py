@@ -21,7 +21,7 @@ from typing import Optional
 
 import torch
 
-from . import NVFP4Error, _check, _dtype_code, _ptr, _stream, load_library
+from . import NVFP4Error, _check, _dtype_code, _stream, load_library
 
 _PAGES = (16, 32, 64, 128, 256)
 _DIMS = (64, 128, 192, 256)
@@ -48,29 +48,29 @@ class KVCache:
     __slots__ = ("k", "v", "k_scales", "v_scales", "pages", "heads", "page", "dim", "device", "index", "_struct", "_ref")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor):
-        if k.dim() != 4:
+        shape, index = k.shape, k.get_device()
+        if len(shape) != 4:
             raise ValueError("k must be [pages, heads, page, dim]")
-        pages, heads, page, dim = k.shape
+        pages, heads, page, dim = shape
+        flat = (pages, heads)
         if v.shape != (pages, heads, dim, page):
-            raise ValueError(f"v {tuple(v.shape)} does not match k {tuple(k.shape)} (expected [pages, heads, dim, page])")
-        if k_scales.shape != (pages, heads) or v_scales.shape != (pages, heads):
+            raise ValueError(f"v {tuple(v.shape)} does not match k {tuple(shape)} (expected [pages, heads, dim, page])")
+        if k_scales.shape != flat or v_scales.shape != flat:
             raise ValueError("k_scales and v_scales must be [pages, heads]")
         if page not in _PAGES or dim not in _DIMS or heads < 1:
             raise ValueError(f"page must be one of {_PAGES}, dim one of {_DIMS} and heads at least 1, "
                              f"got {page}, {dim} and {heads}")
-        index = k.get_device()
-        for t in (k, v, k_scales, v_scales):
-            if t.dtype is not _U8:
-                raise TypeError(f"the cache's tensors must be uint8, got {t.dtype}")
-            if not t.is_contiguous():
-                raise ValueError("the cache's tensors must be contiguous")
-            if t.get_device() != index:
-                raise ValueError("the cache's tensors must be on the same device")
+        if not (k.dtype is _U8 and v.dtype is _U8 and k_scales.dtype is _U8 and v_scales.dtype is _U8):
+            raise TypeError("the cache's tensors must be uint8")
+        if not (k.is_contiguous() and v.is_contiguous() and k_scales.is_contiguous() and v_scales.is_contiguous()):
+            raise ValueError("the cache's tensors must be contiguous")
+        if not index == v.get_device() == k_scales.get_device() == v_scales.get_device():
+            raise ValueError("the cache's tensors must be on the same device")
         if index < 0:
             raise ValueError("the cache's tensors must be on the GPU")
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
-        self.pages, self.heads, self.page, self.dim = pages, heads, page, dim
-        self.device, self.index = k.device, index
+        self.pages, self.heads, self.page, self.dim, self.index = pages, heads, page, dim, index
+        self.device = k.device
         self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
                                     pages, heads, page, dim)
         self._ref = ctypes.addressof(self._struct)
@@ -82,28 +82,22 @@ class KVCache:
         return cls(z(pages, heads, page, dim), z(pages, heads, dim, page), z(pages, heads), z(pages, heads))
 
 
-def _tokens(name: str, x: torch.Tensor, cache: KVCache, heads: Optional[int], tokens: Optional[int], dtype) -> None:
-    """x must be [tokens, heads, dim] on the cache's device with its last axis contiguous."""
-    if x.dim() != 3 or x.shape[2] != cache.dim or (heads is not None and x.shape[1] != heads) or (
-            tokens is not None and x.shape[0] != tokens):
-        raise ValueError(f"{name} {tuple(x.shape)} must be [tokens, heads, dim] with dim {cache.dim}"
-                         + (f", heads {heads}" if heads is not None else "")
-                         + (f", tokens {tokens}" if tokens is not None else ""))
-    if dtype is not None and x.dtype is not dtype:
+# The checks run on every call of a decode step, so each is one comparison of
+# what a call has at hand; what is wrong is worked out only once one fails.
+
+def _refuse_tokens(name: str, x: torch.Tensor, cache: KVCache, tokens: int, heads: int, dtype) -> None:
+    """Raises for a tensor of new tokens that is not [tokens, heads, dim]."""
+    if x.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
+    if x.shape != (tokens, heads, cache.dim):
+        raise ValueError(f"{name} {tuple(x.shape)} must be {(tokens, heads, cache.dim)} ([tokens, heads, dim])")
     if x.get_device() != cache.index:
         raise ValueError(f"{name} must be on the cache's device")
-    if x.stride(2) != 1:
-        raise ValueError(f"{name}'s last axis must be contiguous")
+    raise ValueError(f"{name}'s last axis must be contiguous")
 
 
-def _plan(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, cu_q: Optional[torch.Tensor],
-          max_q: Optional[int], tokens: int):
-    """(batch, width, max_q) of the sequences' tensors, checked."""
-    if table.dim() != 2 or lens.dim() != 1 or lens.shape[0] != table.shape[0]:
-        raise ValueError("table must be [batch, width] and lens [batch]")
-    batch, width = table.shape
-    for name, t in (("table", table), ("lens", lens), ("cu_q", cu_q)):
+def _refuse_sequences(cache: KVCache, **tensors: Optional[torch.Tensor]) -> None:
+    for name, t in tensors.items():
         if t is None:
             continue
         if t.dtype is not _I32:
@@ -112,17 +106,36 @@ def _plan(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, cu_q: Optiona
             raise ValueError(f"{name} must be on the cache's device")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
+    raise ValueError("table must be [batch, width], lens [batch] and cu_q [batch + 1]")
+
+
+def _sequences(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, cu_q: Optional[torch.Tensor],
+               max_q: Optional[int], tokens: int):
+    """(batch, width, max_q, address of cu_q) of the sequences' tensors, checked."""
+    index, shape = cache.index, table.shape
+    if not (len(shape) == 2 and lens.shape == (shape[0],) and table.dtype is _I32 and lens.dtype is _I32
+            and table.get_device() == index == lens.get_device() and table.is_contiguous() and lens.is_contiguous()):
+        _refuse_sequences(cache, table=table, lens=lens)
+    batch, width = shape
     if cu_q is None:
         if tokens != batch:
             raise ValueError(f"without cu_q every sequence has one new token: {tokens} tokens, {batch} sequences")
-        return batch, width, 1
-    if cu_q.dim() != 1 or cu_q.shape[0] != batch + 1:
-        raise ValueError("cu_q must be [batch + 1]")
-    if max_q is None:
-        return batch, width, tokens
-    if max_q < 0 or (max_q == 0 and tokens > 0):
+        return batch, width, 1, None
+    if not (cu_q.shape == (batch + 1,) and cu_q.dtype is _I32 and cu_q.get_device() == index and cu_q.is_contiguous()):
+        _refuse_sequences(cache, cu_q=cu_q)
+    if max_q is None or max_q > tokens:
+        max_q = tokens
+    elif max_q < 0 or (max_q == 0 and tokens > 0):
         raise ValueError("max_q must be at least the new tokens of the longest sequence")
-    return batch, width, min(int(max_q), tokens)
+    return batch, width, max_q, cu_q.data_ptr()
+
+
+def _output(out: Optional[torch.Tensor], q: torch.Tensor, shape, cache: KVCache) -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=q.dtype, device=cache.device)
+    if out.dtype is not q.dtype or out.shape != shape or not out.is_contiguous() or out.get_device() != cache.index:
+        raise ValueError("out must be contiguous, of q's dtype, shape and device")
+    return out
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch.Tensor,
@@ -145,41 +158,47 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, table: torch.Ten
     that it held are then rounded anew; the values of a page at one scale are
     off by at most half a step of their codes.
     """
-    dtype = k.dtype
+    dtype, shape, index, dim = k.dtype, k.shape, cache.index, cache.dim
     code = _dtype_code(dtype)
-    tokens = k.shape[0]
-    _tokens("k", k, cache, cache.heads, None, None)
-    _tokens("v", v, cache, cache.heads, tokens, dtype)
-    batch, width, most = _plan(cache, table, lens, cu_q, max_q, tokens)
-    rot = 0
+    tokens = shape[0] if len(shape) else 0
+    want = (tokens, cache.heads, dim)
+    ks, vs = k.stride(), v.stride()
+    if not (shape == want and k.get_device() == index and (ks[2] == 1 or tokens == 0)):
+        _refuse_tokens("k", k, cache, tokens, cache.heads, dtype)
+    if not (v.shape == want and v.dtype is dtype and v.get_device() == index and (vs[2] == 1 or tokens == 0)):
+        _refuse_tokens("v", v, cache, tokens, cache.heads, dtype)
+    batch, width, most, cu = _sequences(cache, table, lens, cu_q, max_q, tokens)
+    rot, freq = 0, None
     if inv_freq is not None:
-        if inv_freq.dtype is not _F32 or inv_freq.dim() != 1:
-            raise TypeError("inv_freq must be a 1-D float32 tensor")
+        if inv_freq.dtype is not _F32:
+            raise TypeError(f"inv_freq must be float32, got {inv_freq.dtype}")
+        if inv_freq.dim() != 1 or not inv_freq.is_contiguous() or inv_freq.get_device() != index:
+            raise ValueError("inv_freq must be 1-D, contiguous and on the cache's device")
         rot = 2 * inv_freq.shape[0]
-        if rot > cache.dim:
-            raise ValueError(f"inv_freq turns {rot} of {cache.dim} channels")
-        if inv_freq.get_device() != cache.index or not inv_freq.is_contiguous():
-            raise ValueError("inv_freq must be contiguous and on the cache's device")
-        if rot == 0:
-            inv_freq = None
-    heads_q = 0
+        if rot > dim:
+            raise ValueError(f"inv_freq turns {rot} of {dim} channels")
+        freq = inv_freq.data_ptr() if rot else None
     if q is not None:
-        _tokens("q", q, cache, None, tokens, dtype)
-        heads_q = q.shape[1]
-        if out is None:
-            out = torch.empty(q.shape, dtype=dtype, device=cache.device)
-        elif out.dtype is not dtype or out.shape != q.shape or not out.is_contiguous() or out.get_device() != cache.index:
-            raise ValueError("out must be contiguous, of q's dtype, shape and device")
-        q_args = (q.data_ptr(), q.stride(0), q.stride(1), heads_q, out.data_ptr())
+        q_shape = q.shape
+        qs, heads_q = q.stride(), q_shape[1] if len(q_shape) == 3 else 0
+        if not (q_shape == (tokens, heads_q, dim) and q.dtype is dtype and q.get_device() == index
+                and (qs[2] == 1 or tokens == 0 or heads_q == 0)):
+            _refuse_tokens("q", q, cache, tokens, heads_q, dtype)
+        out = _output(out, q, q_shape, cache)
+        qp, q_token, q_head, qo = q.data_ptr(), qs[0], qs[1], out.data_ptr()
     else:
         if out is not None:
             raise ValueError("out without q")
-        q_args = (None, 0, 0, 0, None)
-    if tokens and (q is None or heads_q):
-        _check("nvfp4_kv_append", load_library().nvfp4_kv_append(
-            cache._ref, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), *q_args, code,
-            tokens, _ptr(cu_q), batch, most, table.data_ptr(), width, lens.data_ptr(), _ptr(inv_freq), rot,
-            int(bool(interleaved)), _stream(cache.device)))
+        qp = qo = None
+        q_token = q_head = heads_q = 0
+    if tokens == 0:
+        return out
+    if heads_q == 0:
+        qp = qo = None      # a tensor without heads has no address
+    _check("nvfp4_kv_append", load_library().nvfp4_kv_append(
+        cache._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], qp, q_token, q_head, heads_q, qo, code,
+        tokens, cu, batch, most, table.data_ptr(), width, lens.data_ptr(), freq, rot, 1 if interleaved else 0,
+        _stream(cache.device)))
     return out
 
 
@@ -200,18 +219,20 @@ def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
     zeros for a query that sees nothing.
     """
     code = _dtype_code(q.dtype)
-    _tokens("q", q, cache, None, None, None)
-    tokens, heads_q, dim = q.shape
-    if heads_q % cache.heads != 0:
-        raise ValueError(f"{heads_q} query heads are not a multiple of the cache's {cache.heads}")
-    batch, width, most = _plan(cache, table, lens, cu_q, max_q, tokens)
-    window = int(window)
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=cache.device)
-    elif out.dtype is not q.dtype or out.shape != q.shape or not out.is_contiguous() or out.get_device() != cache.index:
-        raise ValueError("out must be contiguous, of q's dtype, shape and device")
+    shape, heads, dim = q.shape, cache.heads, cache.dim
+    tokens, heads_q = (shape[0], shape[1]) if len(shape) == 3 else (0, 0)
+    qs = q.stride()
+    if not (shape == (tokens, heads_q, dim) and q.get_device() == cache.index
+            and (qs[2] == 1 or tokens == 0 or heads_q == 0)):
+        _refuse_tokens("q", q, cache, tokens, heads_q, q.dtype)
+    if heads_q % heads != 0:
+        raise ValueError(f"{heads_q} query heads are not a multiple of the cache's {heads}")
+    batch, width, most, cu = _sequences(cache, table, lens, cu_q, max_q, tokens)
+    out = _output(out, q, shape, cache)
+    if tokens == 0 or heads_q == 0:
+        return out
     lib = load_library()
-    key = (tokens, heads_q, cache.heads, dim, cache.page, batch, most, width, window, code)
+    key = (tokens, heads_q, heads, dim, cache.page, batch, most, width, window, code)
     ws_bytes = _ATTENTION_WS_CACHE.get(key)
     if ws_bytes is None:
         ws_bytes = int(lib.nvfp4_paged_attention_workspace_size(*key))
@@ -219,12 +240,29 @@ def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
             raise NVFP4Error("nvfp4_paged_attention_workspace_size", ws_bytes)
         if len(_ATTENTION_WS_CACHE) < 4096:
             _ATTENTION_WS_CACHE[key] = ws_bytes
-    ws = torch.empty(ws_bytes, dtype=_U8, device=cache.device) if ws_bytes > 0 else None
+    ws = torch.empty(ws_bytes, dtype=_U8, device=cache.device) if ws_bytes else None
     _check("nvfp4_paged_attention", lib.nvfp4_paged_attention(
-        cache._ref, q.data_ptr(), q.stride(0), q.stride(1), heads_q, code, tokens, _ptr(cu_q), batch, most,
-        table.data_ptr(), width, lens.data_ptr(), window, dim ** -0.5 if scale is None else float(scale), _ptr(ws),
-        ws_bytes, out.data_ptr(), _stream(cache.device)))
+        cache._ref, q.data_ptr(), qs[0], qs[1], heads_q, code, tokens, cu, batch, most, table.data_ptr(), width,
+        lens.data_ptr(), window, dim ** -0.5 if scale is None else scale, ws.data_ptr() if ws_bytes else None, ws_bytes,
+        out.data_ptr(), _stream(cache.device)))
     return out
+
+
+# nvfp4_sample_workspace_size by call shape
+_SAMPLE_WS_CACHE: dict = {}
+
+
+def _row_values(name: str, t: Optional[torch.Tensor], dtype, shape, index: int):
+    """The address of a tensor of one value per row, checked; None for None."""
+    if t is None:
+        return None
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()):
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.get_device() != index:
+            raise ValueError("all tensors must be on the same device")
+        raise ValueError(f"{name} must be contiguous with one value per row")
+    return t.data_ptr()
 
 
 def sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Tensor] = None,
@@ -245,36 +283,39 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Te
     probability among the kept ones, float32 [batch].
     """
     code = _dtype_code(logits.dtype)
-    if logits.dim() != 2:
+    shape, index = logits.shape, logits.get_device()
+    if len(shape) != 2:
         raise ValueError("logits must be [batch, vocab]")
-    batch, vocab = logits.shape
-    index = logits.get_device()
     if index < 0:
         raise ValueError("all tensors must be on the GPU")
-    stride = logits.stride(0) if batch > 1 else vocab
+    batch, vocab = shape
     if vocab == 0 and batch > 0:
         raise ValueError("logits have no tokens")
-    if vocab > 1 and logits.stride(1) != 1 or stride < vocab:
+    row, last = logits.stride()
+    if batch <= 1:
+        row = vocab
+    if (vocab > 1 and last != 1) or row < vocab:
         raise ValueError("logits' last axis must be contiguous and rows must not overlap")
-    for name, t, dtype in (("u", u, _F32), ("temperature", temperature, _F32), ("top_k", top_k, _I32),
-                           ("top_p", top_p, _F32), ("min_p", min_p, _F32)):
-        if t is None:
-            continue
-        if t.dtype is not dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.dim() != 1 or t.shape[0] != batch or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous with one value per row")
-        if t.get_device() != index:
-            raise ValueError("all tensors must be on the same device")
+    per_row = (batch,)
+    up = _row_values("u", u, _F32, per_row, index)
+    tp = _row_values("temperature", temperature, _F32, per_row, index)
+    kp = _row_values("top_k", top_k, _I32, per_row, index)
+    pp = _row_values("top_p", top_p, _F32, per_row, index)
+    mp = _row_values("min_p", min_p, _F32, per_row, index)
     device = logits.device
     token = torch.empty(batch, dtype=_I32, device=device)
     prob = torch.empty(batch, dtype=_F32, device=device) if return_prob else None
     lib = load_library()
-    ws_bytes = int(lib.nvfp4_sample_workspace_size(batch, vocab, code))
-    if ws_bytes < 0:
-        raise NVFP4Error("nvfp4_sample_workspace_size", ws_bytes)
-    ws = torch.empty(ws_bytes, dtype=_U8, device=device) if ws_bytes > 0 else None
+    key = (batch, vocab, code)
+    ws_bytes = _SAMPLE_WS_CACHE.get(key)
+    if ws_bytes is None:
+        ws_bytes = int(lib.nvfp4_sample_workspace_size(*key))
+        if ws_bytes < 0:
+            raise NVFP4Error("nvfp4_sample_workspace_size", ws_bytes)
+        if len(_SAMPLE_WS_CACHE) < 4096:
+            _SAMPLE_WS_CACHE[key] = ws_bytes
+    ws = torch.empty(ws_bytes, dtype=_U8, device=device) if ws_bytes else None
     _check("nvfp4_sample", lib.nvfp4_sample(
-        logits.data_ptr(), code, batch, vocab, stride, u.data_ptr(), _ptr(temperature), _ptr(top_k), _ptr(top_p),
-        _ptr(min_p), _ptr(ws), ws_bytes, token.data_ptr(), _ptr(prob), _stream(device)))
+        logits.data_ptr(), code, batch, vocab, row, up, tp, kp, pp, mp, ws.data_ptr() if ws_bytes else None, ws_bytes,
+        token.data_ptr(), prob.data_ptr() if return_prob else None, _stream(device)))
     return (token, prob) if return_prob else token
