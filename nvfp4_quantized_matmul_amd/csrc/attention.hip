@@ -42,7 +42,8 @@ struct AttnArgs {
   int32_t window;                    // <= 0: none
   int32_t splits, chunk;             // chunk: tokens of a split, a multiple of 64
   int32_t row_tiles;                 // of a sequence and head, at most
-  float scale_log2;                  // scale * log2(e)
+  float scale_log2;                  // |scale| * log2(e)
+  float sign;                        // the scale's: the queries take it
   bool vec;                          // 16-byte loads of q
 };
 
@@ -228,6 +229,8 @@ __global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>:
     if (r < nrows) {
       const int row = row0 + r, t = row / A.group, hh = h * A.group + row % A.group;
       load_row8((const T*)A.q + (int64_t)(sq.row0 + t) * A.q_token + (int64_t)hh * A.q_head + 8 * c8, A.vec, x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] *= A.sign;
     }
     V8 p[PARTS];
     to_parts<T>(x, p);
@@ -560,6 +563,7 @@ struct ManyShared {
   ManyTile<DIM> tile[2];
   GroupInfo info[2][4];
   uint32_t there[2];   // bit g: group g's page is there
+  uint32_t clamped[2]; // some group's rest is not 1
   int32_t nan[2];      // the first token of the last partial tile here that had a NaN code among its values,
   __align__(8) uint16_t nan_tokens[2][DIM][4];   // and which ones: a bit per token
 };
@@ -609,7 +613,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 128 ? 2 : 1) void many_rows
       float x[8];
       load_row8(p + 16 * s, A.vec, x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[s][i] = (E)(my < nrows ? x[i] : 0.0f);
+      for (int i = 0; i < 8; ++i) q[s][i] = (E)(my < nrows ? x[i] * A.sign : 0.0f);
     }
   }
   // positions of the wave's first and last row: rows are in the order of positions
@@ -632,14 +636,35 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 128 ? 2 : 1) void many_rows
     kc[i] = (i * THREADS + tid) % (DIM / 16);
   }
   uint4 kreg[KLOADS], vreg[KLOADS];
-  int idk[KLOADS], idv;
+  int idk[KLOADS], idv = -1;
   int kbyte = 0, vbyte = 0;
+  // A tile inside one page: its page is the block's, and so are the bases of
+  // the loads; a thread's own part of the addresses never changes.
+  const bool one_page = shift >= 6;
+  const uint32_t koff = 16 * tid, voff = (uint32_t)(vch << shift) + 16 * vg;
   auto ids = [&](int t0) {
+    if (one_page) {
+      idv = __builtin_amdgcn_readfirstlane(page_of(t0));
+    } else {
 #pragma unroll
-    for (int i = 0; i < KLOADS; ++i) idk[i] = page_of(t0 + krow[i]);
-    idv = page_of(t0 + 16 * vg);
+      for (int i = 0; i < KLOADS; ++i) idk[i] = page_of(t0 + krow[i]);
+      idv = page_of(t0 + 16 * vg);
+    }
   };
   auto load = [&](int t0) {
+    if (one_page) {
+      const int id = __builtin_amdgcn_readfirstlane(idv);
+      const int64_t ph = (int64_t)(id < 0 ? 0 : id) * A.c.heads + h;
+      const uint8_t* pk = A.c.k + ph * page_bytes + (int64_t)(t0 & pmask) * DIM;
+      const uint8_t* pv = A.c.v + ph * page_bytes + (t0 & pmask);
+#pragma unroll
+      for (int i = 0; i < KLOADS; ++i) kreg[i] = *(const uint4*)(pk + 16 * THREADS * i + koff);
+#pragma unroll
+      for (int i = 0; i < KLOADS; ++i) vreg[i] = *(const uint4*)(pv + ((int64_t)(i * (THREADS / 4)) << shift) + voff);
+      kbyte = A.c.ks[ph];
+      vbyte = A.c.vs[ph];
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < KLOADS; ++i) {
       const int64_t ph = (int64_t)(idk[i] < 0 ? 0 : idk[i]) * A.c.heads + h;
@@ -692,8 +717,11 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 128 ? 2 : 1) void many_rows
       S.info[at][tid] = f;
     }
     if (wave == 0) {
-      const uint64_t there = __ballot(idv >= 0);
-      if (tid == 0) S.there[at] = (uint32_t)there & 0xfu;
+      const uint64_t there = __ballot(idv >= 0), far = __ballot(vbyte < 67 || vbyte > 187);
+      if (tid == 0) {
+        S.there[at] = (uint32_t)there & 0xfu;
+        S.clamped[at] = (uint32_t)far & 0xfu;
+      }
     }
   };
 
@@ -744,29 +772,44 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 128 ? 2 : 1) void many_rows
       }
       const uint32_t there = S.there[at];
       const bool whole = t0 + 63 <= wfirst && (A.window <= 0 || t0 > wlast - A.window) && wave_rows == 32 && there == 0xfu;
-      float top = -__builtin_inff();
+      // the largest score, and the factor and summand that make weights of
+      // scores: of tiles that are seen whole only the largest of each group of
+      // 16 tokens is scaled for it (the factors are not negative)
+      float top = -__builtin_inff(), mul[4], add[4];
       uint64_t vis = ~0ull;   // the tile's tokens that the lane's row sees
-      if (!whole) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        mul[g] = S.info[at][g].kscale;
+        add[g] = S.info[at][g].e;
+      }
+      if (whole) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          float x = sc[g / 2][8 * (g % 2)];
+#pragma unroll
+          for (int j = 1; j < 8; ++j) x = fmaxf(x, sc[g / 2][8 * (g % 2) + j]);
+          top = fmaxf(top, __builtin_fmaf(x, mul[g], add[g]));
+        }
+      } else {
         const int last_i = pos - t0, first_i = A.window > 0 ? pos - A.window + 1 - t0 : 0;
         vis = last_i < 0 ? 0 : last_i >= 63 ? ~0ull : (2ull << last_i) - 1;
         if (first_i > 0) vis = first_i > 63 ? 0 : vis & (~0ull << first_i);
 #pragma unroll
         for (int g = 0; g < 4; ++g) vis &= (there >> g) & 1 ? ~0ull : ~(0xffffull << (16 * g));
-      }
-      const uint32_t seen[2] = {(uint32_t)vis >> (8 * hh), (uint32_t)(vis >> 32) >> (8 * hh)};
+        const uint32_t seen[2] = {(uint32_t)vis >> (8 * hh), (uint32_t)(vis >> 32) >> (8 * hh)};
 #pragma unroll
-      for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const float ck = S.info[at][2 * tt + s].kscale, e = S.info[at][2 * tt + s].e;
+        for (int g = 0; g < 4; ++g) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            float x = __builtin_fmaf(sc[tt][8 * s + j], ck, e);
-            if (!whole) x = (seen[tt] >> (16 * s + j)) & 1 ? x : -__builtin_inff();
-            sc[tt][8 * s + j] = x;
+            float x = __builtin_fmaf(sc[g / 2][8 * (g % 2) + j], mul[g], add[g]);
+            x = (seen[g / 2] >> (16 * (g % 2) + j)) & 1 ? x : -__builtin_inff();
+            sc[g / 2][8 * (g % 2) + j] = x;
             top = fmaxf(top, x);
           }
+          mul[g] = 1.0f;
+          add[g] = 0.0f;
         }
+      }
       top = fmaxf(top, __shfl_xor(top, 32, 64));
       if (__any(top > m + 8.0f)) {
         const float m_new = fmaxf(m, top);
@@ -780,16 +823,26 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 128 ? 2 : 1) void many_rows
       V8 pw[4];
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const float back = S.info[at][g].back, rest = S.info[at][g].rest;
+        const float back = S.info[at][g].back, less = add[g] - base;
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float w = pow2(sc[g / 2][8 * (g % 2) + j] - base);
+          const float w = pow2(__builtin_fmaf(sc[g / 2][8 * (g % 2) + j], mul[g], less));
+          sc[g / 2][8 * (g % 2) + j] = w;
           sum += w;
-          pw[g][j] = (E)(w * rest);
         }
         l = __builtin_fmaf(sum, back, l);
       }
+      if (S.clamped[at]) {   // value scales outside 2^-60 .. 2^60
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sc[g / 2][8 * (g % 2) + j] *= S.info[at][g].rest;
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) pw[g][j] = (E)sc[g / 2][8 * (g % 2) + j];
 #pragma unroll
       for (int c = 0; c < CB; ++c) {
         const int ch = 32 * c + n;
@@ -1029,7 +1082,8 @@ void launch_paged_attention(const nvfp4_kv_cache_t& c, const void* q, int64_t q_
   A.window = window >= width * c.page ? 0 : (int32_t)window;   // a window over the whole table is none
   A.splits = (int32_t)p.splits; A.chunk = (int32_t)p.chunk;
   A.row_tiles = (int32_t)p.row_tiles;
-  A.scale_log2 = scale * kLog2e;
+  A.sign = scale < 0.0f ? -1.0f : 1.0f;
+  A.scale_log2 = scale * A.sign * kLog2e;
   const int64_t size = dt == NVFP4_F32 ? 4 : 2;
   A.vec = ((uintptr_t)q & 15) == 0 && (q_token * size) % 16 == 0 && (q_head * size) % 16 == 0;
   switch (dt) {
