@@ -552,6 +552,12 @@ struct GroupInfo {
   float kscale, e, rest, back;   // score factor; clamped exponent of the values, what the clamp left, 2^-e
 };
 
+// Where the pieces of 16 bytes of row r lie: 16 lanes read a column of pieces
+// of 16 rows in a cycle, 256 bytes of LDS, and meet every bank once.  (With 16
+// pieces a row; 24 are three times the pattern of 8.)
+template <int PIECES>
+__device__ __forceinline__ int swizzle(int r) { return PIECES % 16 == 0 ? r & 15 : (r & 7) ^ ((r >> 3) & 1); }
+
 template <int DIM>
 struct ManyTile {
   uint4 k[64 * DIM / 8];   // [64 rows][DIM / 8] pieces of 8 elements
@@ -568,8 +574,15 @@ struct ManyShared {
   __align__(8) uint16_t nan_tokens[2][DIM][4];   // and which ones: a bit per token
 };
 
-template <typename T, int DIM>
-__global__ __launch_bounds__(64 * kManyWaves, DIM <= 128 ? 2 : 1) void many_rows_kernel(AttnArgs A) {
+// A barrier for what lies in LDS: loads from memory stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+template <typename T, int DIM, bool ONE_PAGE>
+__global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1) void many_rows_kernel(AttnArgs A) {
   typedef typename Mma<T>::V8 V8;
   typedef typename Mma<T>::E E;
   constexpr int KS = DIM / 16, CB = DIM / 32, KP = DIM / 8, THREADS = 64 * kManyWaves;
@@ -635,45 +648,49 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 128 ? 2 : 1) void many_rows
     krow[i] = (i * THREADS + tid) / (DIM / 16);
     kc[i] = (i * THREADS + tid) % (DIM / 16);
   }
+  // Entries of the table are fetched a tile before they are looked at, into
+  // vector registers (a scalar load would be waited for with the next LDS
+  // read), and every load is issued without a branch around it (behind one its
+  // register would be copied, and so waited for, at once): what lies behind
+  // the end reads the last entry, pages that are not there read page 0.
+  // A tile inside one page has one entry, and its addresses are the block's.
+  constexpr int IDS = ONE_PAGE ? 1 : KLOADS + 1, VALUES = IDS - 1;
   uint4 kreg[KLOADS], vreg[KLOADS];
-  int idk[KLOADS], idv = -1;
+  int id[IDS], entry[IDS];   // pages of the keys' loads and of the values', of the next tile; the table's entries of the one after it
   int kbyte = 0, vbyte = 0;
-  // A tile inside one page: its page is the block's, and so are the bases of
-  // the loads; a thread's own part of the addresses never changes.
-  const bool one_page = shift >= 6;
-  const uint32_t koff = 16 * tid, voff = (uint32_t)(vch << shift) + 16 * vg;
-  auto ids = [&](int t0) {
-    if (one_page) {
-      idv = __builtin_amdgcn_readfirstlane(page_of(t0));
-    } else {
+  auto token = [&](int t0, int i) -> int { return ONE_PAGE ? t0 : t0 + (i < KLOADS ? krow[i < KLOADS ? i : 0] : 16 * vg); };
+  auto fetch_ids = [&](int t0) {
 #pragma unroll
-      for (int i = 0; i < KLOADS; ++i) idk[i] = page_of(t0 + krow[i]);
-      idv = page_of(t0 + 16 * vg);
+    for (int i = 0; i < IDS; ++i) {
+      const int t = token(t0, i);
+      int at = (t < hi ? t : hi - 1) >> shift;
+      asm("" : "+v"(at));
+      entry[i] = table[at];
+    }
+  };
+  auto ids = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < IDS; ++i) {
+      id[i] = entry[i] < A.c.pages && token(t0, i) < hi ? entry[i] : -1;
+      if constexpr (ONE_PAGE) id[i] = __builtin_amdgcn_readfirstlane(id[i]);
     }
   };
   auto load = [&](int t0) {
-    if (one_page) {
-      const int id = __builtin_amdgcn_readfirstlane(idv);
-      const int64_t ph = (int64_t)(id < 0 ? 0 : id) * A.c.heads + h;
-      const uint8_t* pk = A.c.k + ph * page_bytes + (int64_t)(t0 & pmask) * DIM;
-      const uint8_t* pv = A.c.v + ph * page_bytes + (t0 & pmask);
-#pragma unroll
-      for (int i = 0; i < KLOADS; ++i) kreg[i] = *(const uint4*)(pk + 16 * THREADS * i + koff);
-#pragma unroll
-      for (int i = 0; i < KLOADS; ++i) vreg[i] = *(const uint4*)(pv + ((int64_t)(i * (THREADS / 4)) << shift) + voff);
-      kbyte = A.c.ks[ph];
-      vbyte = A.c.vs[ph];
-      return;
-    }
 #pragma unroll
     for (int i = 0; i < KLOADS; ++i) {
-      const int64_t ph = (int64_t)(idk[i] < 0 ? 0 : idk[i]) * A.c.heads + h;
-      kreg[i] = *(const uint4*)(A.c.k + ph * page_bytes + (int64_t)((t0 + krow[i]) & pmask) * DIM + 16 * kc[i]);
+      if constexpr (ONE_PAGE) {
+        const uint8_t* base = A.c.k + ((int64_t)(id[0] < 0 ? 0 : id[0]) * A.c.heads + h) * page_bytes + (uint32_t)(t0 & pmask) * DIM;
+        kreg[i] = *(const uint4*)(base + 16 * i * THREADS + 16u * (uint32_t)tid);
+      } else {
+        const int64_t ph = (int64_t)(id[i < IDS ? i : 0] < 0 ? 0 : id[i < IDS ? i : 0]) * A.c.heads + h;
+        kreg[i] = *(const uint4*)(A.c.k + ph * page_bytes + (uint32_t)((t0 + krow[i]) & pmask) * DIM + 16 * kc[i]);
+      }
     }
-    const int64_t ph = (int64_t)(idv < 0 ? 0 : idv) * A.c.heads + h;
-    const uint8_t* p = A.c.v + ph * page_bytes + ((int64_t)vch << shift) + ((t0 + 16 * vg) & pmask);
+    const int64_t ph = (int64_t)(id[VALUES] < 0 ? 0 : id[VALUES]) * A.c.heads + h;
+    const uint8_t* base = A.c.v + ph * page_bytes + (ONE_PAGE ? t0 & pmask : 0);
+    const uint32_t off = (uint32_t)(vch << shift) + (ONE_PAGE ? 16 * vg : (t0 + 16 * vg) & pmask);
 #pragma unroll
-    for (int i = 0; i < KLOADS; ++i) vreg[i] = *(const uint4*)(p + ((int64_t)(i * (THREADS / 4)) << shift));
+    for (int i = 0; i < KLOADS; ++i) vreg[i] = *(const uint4*)(base + ((int64_t)(i * (THREADS / 4)) << shift) + off);
     kbyte = A.c.ks[ph];
     vbyte = A.c.vs[ph];
   };
@@ -701,11 +718,11 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 128 ? 2 : 1) void many_rows
     for (int i = 0; i < KLOADS; ++i) {
       const int tok = krow[i];
       const int r = (tok & 32) | (tok & 16) | ((tok & 4) << 1) | ((tok & 8) >> 1) | (tok & 3);
-      t.k[r * KP + ((2 * kc[i]) ^ (r & 7))] = __builtin_bit_cast(uint4, decode8<V8>(kreg[i].x, kreg[i].y));
-      t.k[r * KP + ((2 * kc[i] + 1) ^ (r & 7))] = __builtin_bit_cast(uint4, decode8<V8>(kreg[i].z, kreg[i].w));
+      t.k[r * KP + ((2 * kc[i]) ^ swizzle<KP>(r))] = __builtin_bit_cast(uint4, decode8<V8>(kreg[i].x, kreg[i].y));
+      t.k[r * KP + ((2 * kc[i] + 1) ^ swizzle<KP>(r))] = __builtin_bit_cast(uint4, decode8<V8>(kreg[i].z, kreg[i].w));
       const int c = vch + i * (THREADS / 4);
-      t.v[c * 8 + ((2 * vg) ^ (c & 7))] = __builtin_bit_cast(uint4, decode8<V8>(vreg[i].x, vreg[i].y));
-      t.v[c * 8 + ((2 * vg + 1) ^ (c & 7))] = __builtin_bit_cast(uint4, decode8<V8>(vreg[i].z, vreg[i].w));
+      t.v[c * 8 + ((2 * vg) ^ swizzle<8>(c))] = __builtin_bit_cast(uint4, decode8<V8>(vreg[i].x, vreg[i].y));
+      t.v[c * 8 + ((2 * vg + 1) ^ swizzle<8>(c))] = __builtin_bit_cast(uint4, decode8<V8>(vreg[i].z, vreg[i].w));
     }
     if (tid < 4) {
       GroupInfo f;
@@ -717,7 +734,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 128 ? 2 : 1) void many_rows
       S.info[at][tid] = f;
     }
     if (wave == 0) {
-      const uint64_t there = __ballot(idv >= 0), far = __ballot(vbyte < 67 || vbyte > 187);
+      const uint64_t there = __ballot(id[VALUES] >= 0), far = __ballot(vbyte < 67 || vbyte > 187);
       if (tid == 0) {
         S.there[at] = (uint32_t)there & 0xfu;
         S.clamped[at] = (uint32_t)far & 0xfu;
@@ -734,26 +751,25 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 128 ? 2 : 1) void many_rows
 
   // a tile is partial for the block if a row does not see it whole or a page is missing
   auto partial = [&](int t0) -> bool {
-    return t0 + 63 > sp.first || (A.window > 0 && t0 <= sp.last - A.window) || t0 + 64 > hi || __any(idv < 0);
+    return t0 + 63 > sp.first || (A.window > 0 && t0 <= sp.last - A.window) || t0 + 64 > hi || __any(id[VALUES] < 0);
   };
 
   if (tid < 2) S.nan[tid] = -1;
   __syncthreads();
   int at = 0;
   if (lo < hi) {
+    fetch_ids(lo);
     ids(lo);
     load(lo);
+    fetch_ids(lo + 64);
     store(0, lo, partial(lo));
     ids(lo + 64);
+    fetch_ids(lo + 128);
   }
   for (int t0 = lo; t0 < hi; t0 += 64, at ^= 1) {
-    __syncthreads();
-    const bool more = t0 + 64 < hi;
-    bool next_partial = false;
-    if (more) {
-      load(t0 + 64);
-      next_partial = partial(t0 + 64);
-    }
+    lds_barrier();
+    load(t0 + 64);   // also behind the last tile, from page 0
+    const bool next_partial = partial(t0 + 64);
     const ManyTile<DIM>& t = S.tile[at];
     const bool unseen = t0 > wlast || (A.window > 0 && t0 + 63 <= wfirst - A.window);
     if (!unseen) {
@@ -767,7 +783,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 128 ? 2 : 1) void many_rows
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt) {
           const int r = 32 * tt + n;
-          sc[tt] = Mma32<T>::mul(__builtin_bit_cast(V8, t.k[r * KP + ((2 * s + hh) ^ (r & 7))]), q[s], sc[tt]);
+          sc[tt] = Mma32<T>::mul(__builtin_bit_cast(V8, t.k[r * KP + ((2 * s + hh) ^ swizzle<KP>(r))]), q[s], sc[tt]);
         }
       }
       const uint32_t there = S.there[at];
@@ -848,7 +864,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 128 ? 2 : 1) void many_rows
         const int ch = 32 * c + n;
 #pragma unroll
         for (int g = 0; g < 4; ++g)
-          o[c] = Mma32<T>::mul(__builtin_bit_cast(V8, t.v[ch * 8 + ((2 * g + hh) ^ (ch & 7))]), pw[g], o[c]);
+          o[c] = Mma32<T>::mul(__builtin_bit_cast(V8, t.v[ch * 8 + ((2 * g + hh) ^ swizzle<8>(ch))]), pw[g], o[c]);
       }
       if (S.nan[at] == t0) {
         // NaN codes lie as zeros in the tile: a channel with one that the row sees is NaN
@@ -861,10 +877,9 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 128 ? 2 : 1) void many_rows
           }
       }
     }
-    if (more) {
-      store(at ^ 1, t0 + 64, next_partial);   // its readers have passed this round's barrier
-      ids(t0 + 128);
-    }
+    store(at ^ 1, t0 + 64, next_partial);   // its readers have passed this round's barrier
+    ids(t0 + 128);
+    fetch_ids(t0 + 192);
   }
 
   l += __shfl_xor(l, 32, 64);
@@ -969,7 +984,7 @@ struct Plan {
 };
 
 Plan make_plan(int64_t heads_q, int64_t heads, int64_t page, int64_t batch, int64_t max_q, int64_t width,
-               int64_t window, nvfp4_dtype_t dt, bool split) {
+               int64_t window, nvfp4_dtype_t dt, int64_t dim, bool split) {
   Plan p;
   const int64_t group = heads_q / heads, rows = max_q * group;
   p.many = dt != NVFP4_F32 && rows > 32;
@@ -988,7 +1003,7 @@ Plan make_plan(int64_t heads_q, int64_t heads, int64_t page, int64_t batch, int6
   if (split) {
     // few rows: three rounds of blocks on the chip, and four tiles a wave at
     // least; many rows: one round, and eight tiles a block
-    const int64_t unit = p.many ? 1 : kFewWaves, least = p.many ? 8 : 4 * kFewWaves, full = p.many ? 512 : 3 * 512;
+    const int64_t unit = p.many ? 1 : kFewWaves, least = p.many ? 8 : 4 * kFewWaves, full = p.many ? (dim <= 64 ? 768 : 512) : 3 * 512;
     int64_t want = p.many ? full / base : (full + base - 1) / base;
     const int64_t most = (tiles + least - 1) / least;
     if (want > most) want = most;
@@ -1017,14 +1032,14 @@ bool launch_few(const AttnArgs& A, int64_t blocks, hipStream_t s) {
   return true;
 }
 
-template <typename T, int DIM>
+template <typename T, int DIM, bool ONE_PAGE>
 bool launch_many(const AttnArgs& A, int64_t blocks, hipStream_t s) {
   constexpr int bytes = (int)sizeof(ManyShared<DIM>);
   static_assert(bytes <= 160 * 1024, "LDS of a workgroup");
   if (bytes > 64 * 1024 &&
-      hipFuncSetAttribute((const void*)many_rows_kernel<T, DIM>, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
+      hipFuncSetAttribute((const void*)many_rows_kernel<T, DIM, ONE_PAGE>, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
     return false;
-  many_rows_kernel<T, DIM><<<dim3((uint32_t)blocks), dim3(64 * kManyWaves), bytes, s>>>(A);
+  many_rows_kernel<T, DIM, ONE_PAGE><<<dim3((uint32_t)blocks), dim3(64 * kManyWaves), bytes, s>>>(A);
   return true;
 }
 
@@ -1032,7 +1047,7 @@ template <typename T, int DIM>
 void launch_dim(const AttnArgs& A, const Plan& p, hipStream_t s) {
   bool ok = false;
   if constexpr (sizeof(T) == 2)
-    if (p.many) ok = launch_many<T, DIM>(A, p.blocks, s);
+    if (p.many) ok = A.c.page_shift >= 6 ? launch_many<T, DIM, true>(A, p.blocks, s) : launch_many<T, DIM, false>(A, p.blocks, s);
   if (!p.many) ok = p.nt == 1 ? launch_few<T, DIM, 1>(A, p.blocks, s) : launch_few<T, DIM, 2>(A, p.blocks, s);
   if (ok && p.splits > 1)
     join_kernel<T, DIM><<<dim3((uint32_t)((int64_t)A.s.tokens * A.heads_q)), dim3(256), 0, s>>>(A, p.rows);
@@ -1054,20 +1069,20 @@ namespace nvfp4host {
 
 int64_t paged_attention_bytes(int64_t tokens, int64_t heads_q, int64_t heads, int64_t dim, int64_t page, int64_t batch,
                               int64_t max_q, int64_t width, int64_t window, nvfp4_dtype_t dt) {
-  return (partials(make_plan(heads_q, heads, page, batch, max_q, width, window, dt, true), tokens, heads_q, dim) + 255) / 256 * 256;
+  return (partials(make_plan(heads_q, heads, page, batch, max_q, width, window, dt, dim, true), tokens, heads_q, dim) + 255) / 256 * 256;
 }
 
-int64_t paged_attention_blocks(int64_t heads_q, int64_t heads, int64_t page, int64_t batch, int64_t max_q, int64_t width,
+int64_t paged_attention_blocks(int64_t heads_q, int64_t heads, int64_t dim, int64_t page, int64_t batch, int64_t max_q, int64_t width,
                                int64_t window, nvfp4_dtype_t dt) {
-  return make_plan(heads_q, heads, page, batch, max_q, width, window, dt, true).blocks;
+  return make_plan(heads_q, heads, page, batch, max_q, width, window, dt, dim, true).blocks;
 }
 
 void launch_paged_attention(const nvfp4_kv_cache_t& c, const void* q, int64_t q_token, int64_t q_head, int64_t heads_q,
                             nvfp4_dtype_t dt, int64_t tokens, const int32_t* cu, int64_t batch, int64_t max_q,
                             const int32_t* table, int64_t width, const int32_t* lens, int64_t window, float scale,
                             void* ws, int64_t ws_bytes, void* out, hipStream_t s) {
-  Plan p = make_plan(heads_q, c.heads, c.page, batch, max_q, width, window, dt, true);
-  if (ws_bytes < partials(p, tokens, heads_q, c.dim)) p = make_plan(heads_q, c.heads, c.page, batch, max_q, width, window, dt, false);
+  Plan p = make_plan(heads_q, c.heads, c.page, batch, max_q, width, window, dt, c.dim, true);
+  if (ws_bytes < partials(p, tokens, heads_q, c.dim)) p = make_plan(heads_q, c.heads, c.page, batch, max_q, width, window, dt, c.dim, false);
   AttnArgs A;
   A.c = {c.k, c.v, c.k_scales, c.v_scales, (int32_t)c.pages, (int32_t)c.heads, __builtin_ctz((unsigned)c.page)};
   A.s = {table, lens, cu, width, (int32_t)batch, (int32_t)tokens};

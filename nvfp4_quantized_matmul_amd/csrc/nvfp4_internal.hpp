@@ -138,7 +138,7 @@ void launch_kv_append(const nvfp4_kv_cache_t& c, const void* k, int64_t k_token,
 // a split of the token axis wants (0: none), paged_attention_blocks its grid.
 int64_t paged_attention_bytes(int64_t tokens, int64_t heads_q, int64_t heads, int64_t dim, int64_t page, int64_t batch,
                               int64_t max_q, int64_t width, int64_t window, nvfp4_dtype_t dt);
-int64_t paged_attention_blocks(int64_t heads_q, int64_t heads, int64_t page, int64_t batch, int64_t max_q, int64_t width,
+int64_t paged_attention_blocks(int64_t heads_q, int64_t heads, int64_t dim, int64_t page, int64_t batch, int64_t max_q, int64_t width,
                                int64_t window, nvfp4_dtype_t dt);
 void launch_paged_attention(const nvfp4_kv_cache_t& c, const void* q, int64_t q_token, int64_t q_head, int64_t heads_q,
                             nvfp4_dtype_t dt, int64_t tokens, const int32_t* cu, int64_t batch, int64_t max_q,

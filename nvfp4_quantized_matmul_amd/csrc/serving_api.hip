@@ -164,7 +164,7 @@ int nvfp4_paged_attention(const nvfp4_kv_cache_t* cache, const void* q, int64_t 
                     overlaps(workspace, workspace_bytes, cache->k, cache_bytes) ||
                     overlaps(workspace, workspace_bytes, cache->v, cache_bytes)))
     return NVFP4_ERR_SHAPE;
-  if (nvfp4host::paged_attention_blocks(heads_q, cache->heads, cache->page, batch, max_q, table_width, window, dtype) >
+  if (nvfp4host::paged_attention_blocks(heads_q, cache->heads, cache->dim, cache->page, batch, max_q, table_width, window, dtype) >
       nvfp4host::kMaxGridX)
     return NVFP4_ERR_GRID;
   nvfp4host::launch_paged_attention(*cache, q, q_token, q_head, heads_q, dtype, tokens, cu_q, batch, max_q, table,
