@@ -859,13 +859,14 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1
       for (int g = 0; g < 4; ++g)
 #pragma unroll
         for (int j = 0; j < 8; ++j) pw[g][j] = (E)sc[g / 2][8 * (g % 2) + j];
+      // one multiply after the other into different sums: into the same one it would wait
 #pragma unroll
-      for (int c = 0; c < CB; ++c) {
-        const int ch = 32 * c + n;
+      for (int g = 0; g < 4; ++g)
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
+        for (int c = 0; c < CB; ++c) {
+          const int ch = 32 * c + n;
           o[c] = Mma32<T>::mul(__builtin_bit_cast(V8, t.v[ch * 8 + ((2 * g + hh) ^ swizzle<8>(ch))]), pw[g], o[c]);
-      }
+        }
       if (S.nan[at] == t0) {
         // NaN codes lie as zeros in the tile: a channel with one that the row sees is NaN
 #pragma unroll
