@@ -257,16 +257,15 @@ __global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>:
   const int32_t* table = A.s.table + (int64_t)b * A.s.width;
   const int64_t page_bytes = (int64_t)DIM << shift;
 
-  // the page of token t; -1 where it is not there
-  auto page_of = [&](int t) -> int {
-    if (t >= hi) return -1;
-    const int id = table[t >> shift];
-    return id < A.c.pages ? id : -1;
-  };
+  // The table's entry of token t (behind the end: the last one), and the page
+  // that it means there; -1 where there is none.  Entries are fetched a tile
+  // ahead and no load stands behind a branch: waiting for either at once would
+  // wait for every load of codes before it.
+  auto entry_of = [&](int t) -> int { return table[(t < hi ? t : hi - 1) >> shift]; };
+  auto page_of = [&](int entry, int t) -> int { return entry < A.c.pages && t < hi ? entry : -1; };
 
   constexpr int STEP = 64 * kFewWaves;
   uint4 kreg[4][U], vreg[CB];
-  int idv_next = -1;
   float kscale = 0.0f, vexp = 0.0f;
   int kbyte = 0, vbyte = 0;
 
@@ -289,18 +288,25 @@ __global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>:
   };
 
   int t0 = lo + wave * 64;
-  int idk = -1, idv = -1;
+  const int tk = (n >> 2) * 16, tv = g * 16;   // the lane's first tokens of a tile, of keys and of values
+  int idk = -1, idv = -1, entry_k = -1, entry_v = -1;
   if (t0 < hi) {
-    idk = page_of(t0 + (n >> 2) * 16);
-    idv = page_of(t0 + g * 16);
+    idk = page_of(entry_of(t0 + tk), t0 + tk);
+    idv = page_of(entry_of(t0 + tv), t0 + tv);
+    entry_k = entry_of(t0 + STEP + tk);
+    entry_v = entry_of(t0 + STEP + tv);
     load_k(t0, idk);
     load_v(t0, idv);
   }
   for (; t0 < hi; t0 += STEP) {
     const int t_next = t0 + STEP;
     asm volatile("" ::: "memory");   // the query operands are read from LDS in each tile: held, they would fill the registers
-    const int idk_next = page_of(t_next + (n >> 2) * 16);
-    idv_next = page_of(t_next + g * 16);
+    // behind the last tile that one is loaded again
+    const bool more = t_next < hi;
+    const int t_load = more ? t_next : t0;
+    const int idk_next = more ? page_of(entry_k, t_next + tk) : idk, idv_next = more ? page_of(entry_v, t_next + tv) : idv;
+    entry_k = entry_of(t_next + STEP + tk);
+    entry_v = entry_of(t_next + STEP + tv);
     kscale = __builtin_ldexpf(A.scale_log2, kbyte - 127);
     vexp = (float)(vbyte - 127);
 
@@ -327,11 +333,11 @@ __global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>:
           }
       }
     }
-    if (t_next < hi) load_k(t_next, idk_next);
+    load_k(t_load, idk_next);
 
     // what each row sees; a tile that all rows see whole needs no comparison
     const bool whole = t0 + 63 <= sp.first && (A.window <= 0 || t0 > sp.last - A.window) && t0 + 64 <= hi &&
-                       nrows == ROWS && __all(idv >= 0);
+                       __all(idv >= 0);   // columns without a row may hold anything
     float e = vexp < -60.0f ? -60.0f : vexp > 60.0f ? 60.0f : vexp;
     const float rest = pow2(vexp - e), back = pow2(-e);
     V8 pw[NT][2][PARTS];
@@ -350,21 +356,33 @@ __global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>:
           for (int i = 0; i < 16; ++i) seen[nt] |= (i <= last_i && i >= first_i) ? 1u << i : 0u;
         }
       }
-      float w[16], top = -__builtin_inff();
+      // a lane's tokens share their scales: of a tile that is seen whole only
+      // the largest score is scaled for the maximum (the factor is not negative)
+      float w[16], top, mul = kscale, add = e;
+      if (whole) {
+        top = sc[nt][0][0];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        w[i] = __builtin_fmaf(sc[nt][i / 4][i % 4], kscale, e);
-        if (!whole) w[i] = (seen[nt] >> i) & 1 ? w[i] : -__builtin_inff();
-        top = fmaxf(top, w[i]);
+        for (int i = 1; i < 16; ++i) top = fmaxf(top, sc[nt][i / 4][i % 4]);
+        top = __builtin_fmaf(top, mul, add);
+      } else {
+        top = -__builtin_inff();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float x = (seen[nt] >> i) & 1 ? __builtin_fmaf(sc[nt][i / 4][i % 4], kscale, e) : -__builtin_inff();
+          sc[nt][i / 4][i % 4] = x;
+          top = fmaxf(top, x);
+        }
+        mul = 1.0f;
+        add = 0.0f;
       }
       const float m_new = fmaxf(m[nt], max_across_groups(top));
       const float base = m_new == -__builtin_inff() ? 0.0f : m_new;
-      const float alpha = pow2(m[nt] - base);
+      const float alpha = pow2(m[nt] - base), less = add - base;
       m[nt] = m_new;
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        w[i] = pow2(w[i] - base);
+        w[i] = pow2(__builtin_fmaf(sc[nt][i / 4][i % 4], mul, less));
         sum += w[i];
       }
       l[nt] = __builtin_fmaf(sum, back, l[nt] * alpha);
@@ -429,7 +447,7 @@ __global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>:
           for (int i = 0; i < 4; ++i) o[nt][c][i] = hits[nt][i] > 0.0f ? __builtin_nanf("") : o[nt][c][i];
       }
     }
-    if (t_next < hi) load_v(t_next, idv_next);
+    load_v(t_load, idv_next);
     idk = idk_next;
     idv = idv_next;
   }
@@ -954,6 +972,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs A, int rows_per_tile
   float acc[DIM / 64], l = 0.0f;
 #pragma unroll
   for (int c = 0; c < DIM / 64; ++c) acc[c] = 0.0f;
+#pragma unroll 4
   for (int i = wave; i < n; i += 4) {
     const float f = pow2(pm[i] - base);
     l = __builtin_fmaf(pl[i], f, l);
