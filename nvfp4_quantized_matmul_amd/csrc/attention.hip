@@ -1114,7 +1114,7 @@ void launch_paged_attention(const nvfp4_kv_cache_t& c, const void* q, int64_t q_
   A.part_m = p.splits > 1 ? A.part_o + prow * c.dim : nullptr;
   A.part_l = p.splits > 1 ? A.part_m + prow : nullptr;
   A.heads_q = (int32_t)heads_q; A.group = (int32_t)(heads_q / c.heads);
-  A.window = window >= width * c.page ? 0 : (int32_t)window;   // a window over the whole table is none
+  A.window = window <= 0 || window >= width * c.page ? 0 : (int32_t)window;   // a window over the whole table is none
   A.splits = (int32_t)p.splits; A.chunk = (int32_t)p.chunk;
   A.row_tiles = (int32_t)p.row_tiles;
   A.sign = scale < 0.0f ? -1.0f : 1.0f;
