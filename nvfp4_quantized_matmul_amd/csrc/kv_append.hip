@@ -27,8 +27,8 @@ constexpr int kThreads = 256;
 // Rotated items that a thread keeps between the two passes over a page (16
 // values each): 4 hold a page of 16384 values, what is over is rotated twice.
 constexpr int kHeld = 4;
-// Tokens of a query block.
-constexpr int kTokensWide = 4;
+// Tokens of a query block, and items that a thread loads before it turns them.
+constexpr int kTokensWide = 4, kQueryItems = 3;
 
 struct AppendArgs {
   CacheView c;
@@ -376,24 +376,40 @@ __device__ void rotate_queries(const AppendArgs& A, int64_t block, double2* turn
   }
   __syncthreads();
   const int per = A.dim / (2 * W), turning = A.rot / (2 * W), row_items = A.heads_q * per;
-  for (int it = threadIdx.x; it < n * row_items; it += kThreads) {
-    const int t = it / row_items, rest = it - t * row_items;
-    const int h = rest / per, j = rest - h * per;
-    int ca, cb;
-    item_channels<W, INTER>(j, A.rot, &ca, &cb);
-    const T* row = (const T*)A.q + (int64_t)(t0 + t) * A.q_token + (int64_t)h * A.q_head;
-    float a[W], b[W];
-    load_group<T, W>(row + ca, a);
-    load_group<T, W>(row + cb, b);
-    if (j < turning)
-      rotate_item<W, INTER>(a, b, [&](int i, double* sn, double* cs) {
-        const double2 d = turn[t * half + W * j + i];
-        *sn = d.x;
-        *cs = d.y;
-      });
-    T* out = (T*)A.q_out + ((int64_t)(t0 + t) * A.heads_q + h) * A.dim;
-    store_group<T, W>(out + ca, a);
-    store_group<T, W>(out + cb, b);
+  // the loads of several items in flight at a time
+  const int all = n * row_items;
+  for (int it0 = threadIdx.x; it0 < all; it0 += kQueryItems * kThreads) {
+    float a[kQueryItems][W], b[kQueryItems][W];
+#pragma unroll
+    for (int r = 0; r < kQueryItems; ++r) {
+      const int it = it0 + r * kThreads;
+      if (it < all) {
+        const int t = it / row_items, rest = it - t * row_items, h = rest / per;
+        int ca, cb;
+        item_channels<W, INTER>(rest - h * per, A.rot, &ca, &cb);
+        const T* row = (const T*)A.q + (int64_t)(t0 + t) * A.q_token + (int64_t)h * A.q_head;
+        load_group<T, W>(row + ca, a[r]);
+        load_group<T, W>(row + cb, b[r]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kQueryItems; ++r) {
+      const int it = it0 + r * kThreads;
+      if (it < all) {
+        const int t = it / row_items, rest = it - t * row_items, h = rest / per, j = rest - h * per;
+        int ca, cb;
+        item_channels<W, INTER>(j, A.rot, &ca, &cb);
+        if (j < turning)
+          rotate_item<W, INTER>(a[r], b[r], [&](int i, double* sn, double* cs) {
+            const double2 d = turn[t * half + W * j + i];
+            *sn = d.x;
+            *cs = d.y;
+          });
+        T* out = (T*)A.q_out + ((int64_t)(t0 + t) * A.heads_q + h) * A.dim;
+        store_group<T, W>(out + ca, a[r]);
+        store_group<T, W>(out + cb, b[r]);
+      }
+    }
   }
 }
 
