@@ -934,13 +934,17 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1
 }
 
 // ---------------------------------------------------------------------------
-// Join of a split axis: a block per output row
+// Join of a split axis
 // ---------------------------------------------------------------------------
-template <typename T, int DIM>
+//
+// WAVES waves per output row, four or one: with few splits there are many
+// rows, and a block's start and sums through LDS cost more than its loads.
+template <typename T, int DIM, int WAVES>
 __global__ __launch_bounds__(256) void join_kernel(AttnArgs A, int rows_per_tile) {
   __shared__ float sum_o[4][DIM];
   __shared__ float sum_l[4];
-  const int64_t at = blockIdx.x;
+  const int64_t at = WAVES == 4 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (at >= (int64_t)A.s.tokens * A.heads_q) return;
   const int t_abs = (int)(at / A.heads_q), hh = (int)(at % A.heads_q);
   int b = t_abs;
   if (A.s.cu) {
@@ -973,12 +977,17 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs A, int rows_per_tile
 #pragma unroll
   for (int c = 0; c < DIM / 64; ++c) acc[c] = 0.0f;
 #pragma unroll 4
-  for (int i = wave; i < n; i += 4) {
+  for (int i = WAVES == 4 ? wave : 0; i < n; i += WAVES) {
     const float f = pow2(pm[i] - base);
     l = __builtin_fmaf(pl[i], f, l);
     const float* po = A.part_o + (at * A.splits + i) * DIM;
 #pragma unroll
     for (int c = 0; c < DIM / 64; ++c) acc[c] = __builtin_fmaf(po[c * 64 + lane], f, acc[c]);
+  }
+  if constexpr (WAVES == 1) {
+#pragma unroll
+    for (int c = 0; c < DIM / 64; ++c) store_out((T*)A.out + at * DIM + c * 64 + lane, l == 0.0f ? 0.0f : acc[c] / l);
+    return;
   }
 #pragma unroll
   for (int c = 0; c < DIM / 64; ++c) sum_o[wave][c * 64 + lane] = acc[c];
@@ -1069,8 +1078,11 @@ void launch_dim(const AttnArgs& A, const Plan& p, hipStream_t s) {
   if constexpr (sizeof(T) == 2)
     if (p.many) ok = A.c.page_shift >= 6 ? launch_many<T, DIM, true>(A, p.blocks, s) : launch_many<T, DIM, false>(A, p.blocks, s);
   if (!p.many) ok = p.nt == 1 ? launch_few<T, DIM, 1>(A, p.blocks, s) : launch_few<T, DIM, 2>(A, p.blocks, s);
-  if (ok && p.splits > 1)
-    join_kernel<T, DIM><<<dim3((uint32_t)((int64_t)A.s.tokens * A.heads_q)), dim3(256), 0, s>>>(A, p.rows);
+  if (ok && p.splits > 1) {
+    const int64_t out_rows = (int64_t)A.s.tokens * A.heads_q;
+    if (p.splits <= 16) join_kernel<T, DIM, 1><<<dim3((uint32_t)((out_rows + 3) / 4)), dim3(256), 0, s>>>(A, p.rows);
+    else join_kernel<T, DIM, 4><<<dim3((uint32_t)out_rows), dim3(256), 0, s>>>(A, p.rows);
+  }
 }
 
 template <typename T>
