@@ -11,14 +11,14 @@
 // where most logits are equal, and one with an infinite largest logit are
 // searched by the bits of the logit instead, in one block (row_by_digits).
 //
-// A row of at most eight rounds of its block's 16-byte loads runs in one
-// block and launch: latency counts there.  Longer ones are cut into tiles of
-// that size, or smaller while blocks are few, in up to five launches (range,
-// histogram, gathering, sums, choice).
+// A row of at most eight rounds of its block's 16-byte loads runs in one block
+// and launch if top-k or top-p are asked for: latency counts there.  Others are
+// cut into tiles of that size, or smaller while blocks are few, in three or
+// five launches (range; histogram and gathering; sums; choice).
 //
 // Bound by the vector units, 64-bit arithmetic most of it: one row of 32000
 // float32 logits with all filters 39 us (the search by digits in one block 53
-// us), 64 rows of 262144 bf16 logits 109 us (488 us), of which reading them
+// us), 16 rows of 50001 f16 logits with min-p 20 us, 64 rows of 262144 bf16 logits 109 us (488 us), of which reading them
 // once would be 7: 8 for the range, 30 for the histogram, 28 for gathering, 36
 // for the sums, 11 for the choice.
 //
@@ -1124,22 +1124,34 @@ void tiling(int64_t batch, int64_t vocab, int64_t stripe, int64_t* tiles, int64_
   *tiles = (rounds + s - 1) / s;
 }
 
+// Whether each row runs in one block.  With top-k or top-p five launches are
+// not faster before a block's eight rounds are over (32000 float32 logits: 39
+// us both ways; 64 such rows 43 us in one block each, 61 us in tiles); without,
+// three launches are, from the third round on (16 rows of 50001 f16 logits 20
+// us, 35 us in one block each), until the rows alone fill half of the chip.
+bool by_rows(int64_t batch, int64_t vocab, int64_t stripe, bool ordered) {
+  const int64_t rounds = (vocab + stripe - 1) / stripe;
+  return rounds <= (ordered || batch >= 128 ? kStripes : 2);
+}
+
 template <typename T>
 void launch(const SampleArgs& A, int64_t batch, uint8_t* ws, int64_t ws_bytes, hipStream_t s) {
-  if (A.vocab <= kStripes * kStripe<T>) {
+  const bool ordered = A.top_k || A.top_p;
+  int64_t tiles, stripes;
+  tiling(batch, A.vocab, kStripe<T>, &tiles, &stripes);
+  SplitArgs P{ws, row_work_bytes(tiles, stripes), (int32_t)tiles, (int32_t)stripes, ordered};
+  const bool room = tiles <= kMaxTiles && ws_bytes >= batch * P.row_bytes;
+  if (by_rows(batch, A.vocab, kStripe<T>, ordered) || (!room && A.vocab <= kStripes * kStripe<T>)) {
     sample_row_kernel<T><<<dim3((uint32_t)batch), dim3(kThreads), 0, s>>>(A);
     return;
   }
-  int64_t tiles, stripes;
-  tiling(batch, A.vocab, kStripe<T>, &tiles, &stripes);
-  SplitArgs P{ws, row_work_bytes(tiles, stripes), (int32_t)tiles, (int32_t)stripes, A.top_k || A.top_p};
-  if (tiles > kMaxTiles || ws_bytes < batch * P.row_bytes) {
+  if (!room) {
     sample_digits_kernel<T><<<dim3((uint32_t)batch), dim3(kThreads), 0, s>>>(A);
     return;
   }
   const dim3 grid((uint32_t)tiles, (uint32_t)batch), one(1, (uint32_t)batch);
   sample_phase_kernel<T, kRange><<<grid, dim3(kThreads), 0, s>>>(A, P);
-  if (P.ordered) {
+  if (ordered) {
     sample_phase_kernel<T, kHistogram><<<grid, dim3(kThreads), 0, s>>>(A, P);
     sample_phase_kernel<T, kGather><<<grid, dim3(kThreads), 0, s>>>(A, P);
   }
@@ -1149,7 +1161,7 @@ void launch(const SampleArgs& A, int64_t batch, uint8_t* ws, int64_t ws_bytes, h
 
 template <typename T>
 int64_t bytes_of(int64_t batch, int64_t vocab) {
-  if (vocab <= kStripes * kStripe<T>) return 0;
+  if (by_rows(batch, vocab, kStripe<T>, false)) return 0;
   int64_t tiles, stripes;
   tiling(batch, vocab, kStripe<T>, &tiles, &stripes);
   return tiles > kMaxTiles ? 0 : batch * row_work_bytes(tiles, stripes);

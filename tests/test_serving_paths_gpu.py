@@ -85,6 +85,18 @@ def test_sample_without_a_workspace():
     assert lib.nvfp4_sample(x.data_ptr(), 1, 2, 120000, 120000, u.data_ptr(), None, k.data_ptr(), p.data_ptr(), None,
                             None, 0, token.data_ptr(), None, stream) == 0
     assert torch.equal(token, want)
+    want = nv.sample(x[:, :50000], u)            # tiles with one, a block without
+    assert lib.nvfp4_sample(x.data_ptr(), 1, 2, 50000, 120000, u.data_ptr(), None, None, None, None, None, 0,
+                            token.data_ptr(), None, stream) == 0
+    assert torch.equal(token, want)
+
+
+def test_sample_min_p_above_one_in_tiles():
+    """Alone, without top-k and top-p: the first of the largest logits stays."""
+    g = torch.Generator().manual_seed(52)
+    x = torch.randn(3, 60000, generator=g)
+    x[1, 30000], x[1, 50000] = 9.0, 9.0
+    run_sample(x, [0.1, 0.9, 0.5], m=[1.5, 1.001, 0.5])
 
 
 def test_sample_in_a_graph():
