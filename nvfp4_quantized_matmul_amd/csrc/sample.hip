@@ -720,16 +720,15 @@ __device__ void tile_gather(const T* row, int from, int to, const Bins& b, Fast&
   logits_of_bins(b, lo, hi, &from_p, &to_p);
   logits_of_bins(b, bk, bk < kNB ? bk : -1, &from_k, &to_k);
   each_piece<T>(row, from, to, [&](Piece<T>& p, int i0) {
+    const auto near = [&](float x) { return (x >= from_p && x <= to_p) || (x >= from_k && x <= to_k); };
     bool any = false;
 #pragma unroll
-    for (int e = 0; e < kVec<T>; ++e) {
-      const float x = p.raw(e);
-      any |= (x >= from_p && x <= to_p) || (x >= from_k && x <= to_k);
-    }
+    for (int e = 0; e < kVec<T>; ++e) any |= near(p.raw(e));
     if (!any) return;
 #pragma unroll 1
     for (int e = 0; e < kVec<T>; ++e) {
       const float x = p.take();
+      if (!near(x)) continue;
       const double y = distance(b, x);
       const int bin = y <= kFar ? bin_of(b, y) : kNB;
       if ((bin >= lo && bin <= hi) || (bin == bk && bk < kNB)) {
@@ -847,7 +846,10 @@ __device__ void tile_sums(const T* row, int from, int to, const Bins& b, unsigne
     for (int e = 0; e < kVec<T>; ++e) any |= p.raw(e) >= least;
     if (!any) return;
 #pragma unroll 1
-    for (int e = 0; e < kVec<T>; ++e) sum += kept_weight(b, last, floor_w, p.take(), i0 + e);
+    for (int e = 0; e < kVec<T>; ++e) {
+      const float x = p.take();
+      if (x >= least) sum += kept_weight(b, last, floor_w, x, i0 + e);
+    }
   }, [&](int j) {
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
@@ -1010,10 +1012,19 @@ __device__ __forceinline__ RowWork row_work(const SplitArgs& P, int row) {
 }
 
 __device__ __forceinline__ Bins split_bins(const SplitArgs& P, const RowWork& w, double rate) {
+  static_assert(kMaxTiles <= 64, "a lane per tile");
+  const int lane = threadIdx.x & 63;
   float top = -__builtin_inff(), least = __builtin_inff();
-  for (int i = 0; i < P.tiles; ++i) top = fmaxf(top, w.range[2 * i]);
-  // a tile's least counts only if the tile has any
-  for (int i = 0; i < P.tiles; ++i) least = w.range[2 * i] > -__builtin_inff() ? fminf(least, w.range[2 * i + 1]) : least;
+  if (lane < P.tiles) {
+    const float2 r = *(const float2*)(w.range + 2 * lane);
+    top = r.x;
+    least = top > -__builtin_inff() ? r.y : least;   // a tile without a token has no least one
+  }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) {
+    top = fmaxf(top, __shfl_xor(top, off, 64));
+    least = fminf(least, __shfl_xor(least, off, 64));
+  }
   return bins_of(top, least, rate);
 }
 
@@ -1022,6 +1033,7 @@ __device__ __forceinline__ void split_borders(const SplitArgs& P, const RowWork&
   uint32_t n[2] = {0, 0};
   unsigned long long deficit[2] = {0, 0};
   const unsigned long long mask = (1ull << kCountBit) - 1;
+#pragma unroll 4
   for (int i = 0; i < P.tiles; ++i) {
     const ulonglong2 h = *(const ulonglong2*)(w.hist + (int64_t)i * kNB + 2 * threadIdx.x);
     n[0] += (uint32_t)(h.x >> kCountBit);
