@@ -180,7 +180,7 @@ __device__ __forceinline__ Span span_of(const AttnArgs& A, const Sequence& s, in
 // between waves until the end, so K and V go straight from memory to
 // registers; the queries lie in LDS as operands.
 //
-// Bound by memory: 4 sequences of up to 128k tokens (837 MB) take 164 us, 5.1
+// Bound by memory: 4 sequences of up to 128k tokens (837 MB) take 165 us, 5.1
 // TB/s, where a copy of 2 GiB reaches 4.95; 32 of up to 8k 28 us, 3.1 TB/s and
 // 4 us of it the join.  Loads that bypass the caches took 193 us for the
 // former: in pages of 128 tokens two waves share each line of the values.
@@ -558,8 +558,8 @@ __global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>:
 // exponentials, 16 maxima, 32 scalings, 32 sums and 16 conversions a lane
 // (about 1100 cycles) to 1024 (dim 128) or 512 (dim 64) of multiplies, and two
 // or three waves a SIMD overlap them in part.  A causal prompt of 4096 tokens,
-// 42 heads of 128, takes 243 us (742 TFLOP/s); 1024 tokens over 32768, 16
-// heads of 64, 226 us (597 TFLOP/s).  Two groups of four waves that took turns
+// 42 heads of 128, takes 244 us (740 TFLOP/s); 1024 tokens over 32768, 16
+// heads of 64, 229 us (591 TFLOP/s).  Two groups of four waves that took turns
 // at multiplies and weights over the same tile measured 256 and 273 us.
 constexpr int kManyWaves = 4, kManyRows = 32 * kManyWaves;
 

@@ -17,9 +17,9 @@
 // five launches (range; histogram and gathering; sums; choice).
 //
 // Bound by the vector units, 64-bit arithmetic most of it: one row of 32000
-// float32 logits with all filters 39 us (the search by digits in one block 53
-// us), 16 rows of 50001 f16 logits with min-p 20 us, 64 rows of 262144 bf16 logits 109 us (488 us), of which reading them
-// once would be 7: 8 for the range, 30 for the histogram, 28 for gathering, 36
+// float32 logits with all filters 40 us (the search by digits in one block 53
+// us), 16 rows of 50001 f16 logits with min-p 19 us, 64 rows of 262144 bf16 logits 106 us (488 us), of which reading them
+// once would be 7: 8 for the range, 28 for the histogram, 28 for gathering, 34
 // for the sums, 11 for the choice.
 //
 // With a quarter of a million tokens a probability is a millionth and the
@@ -1139,7 +1139,7 @@ void tiling(int64_t batch, int64_t vocab, int64_t stripe, int64_t* tiles, int64_
 // Whether each row runs in one block.  With top-k or top-p five launches are
 // not faster before a block's eight rounds are over (32000 float32 logits: 39
 // us both ways; 64 such rows 43 us in one block each, 61 us in tiles); without,
-// three launches are, from the third round on (16 rows of 50001 f16 logits 20
+// three launches are, from the third round on (16 rows of 50001 f16 logits 19
 // us, 35 us in one block each), until the rows alone fill half of the chip.
 bool by_rows(int64_t batch, int64_t vocab, int64_t stripe, bool ordered) {
   const int64_t rounds = (vocab + stripe - 1) / stripe;
