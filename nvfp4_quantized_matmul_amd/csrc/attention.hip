@@ -140,6 +140,10 @@ __device__ __forceinline__ void load_row8(const T* row, bool vec, float (&x)[8])
   }
 }
 
+// Scaled scores of this size are rounded by 1/16 and more, so weights have to
+// come from the same roundings as the maximum.
+__device__ __forceinline__ bool huge_score(float x) { return __builtin_fabsf(x) > 1048576.0f; }
+
 __device__ __forceinline__ float pow2(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float max_across_groups(float v) {
   v = fmaxf(v, __shfl_xor(v, 16, 64));
@@ -362,14 +366,18 @@ __global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>:
         }
       }
       // a lane's tokens share their scales: of a tile that is seen whole only
-      // the largest score is scaled for the maximum (the factor is not negative)
+      // the largest score is scaled for the maximum (the factor is not
+      // negative).  Float32 leaves no registers for both ways.
       float w[16], top, mul = kscale, add = e;
-      if (whole) {
+      bool scaled = PARTS > 1 || !whole;
+      if (PARTS == 1 && whole) {
         top = sc[nt][0][0];
 #pragma unroll
         for (int i = 1; i < 16; ++i) top = fmaxf(top, sc[nt][i / 4][i % 4]);
         top = __builtin_fmaf(top, mul, add);
-      } else {
+        scaled = __any(huge_score(top));
+      }
+      if (scaled) {
         top = -__builtin_inff();
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -829,6 +837,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1
         mul[g] = S.info[at][g].kscale;
         add[g] = S.info[at][g].e;
       }
+      bool scaled = !whole;
       if (whole) {
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -837,7 +846,10 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1
           for (int j = 1; j < 8; ++j) x = fmaxf(x, sc[g / 2][8 * (g % 2) + j]);
           top = fmaxf(top, __builtin_fmaf(x, mul[g], add[g]));
         }
-      } else {
+        scaled = __any(huge_score(top));
+      }
+      if (scaled) {
+        top = -__builtin_inff();
         const int last_i = pos - t0, first_i = A.window > 0 ? pos - A.window + 1 - t0 : 0;
         vis = last_i < 0 ? 0 : last_i >= 63 ? ~0ull : (2ull << last_i) - 1;
         if (first_i > 0) vis = first_i > 63 ? 0 : vis & (~0ull << first_i);
