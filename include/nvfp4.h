@@ -491,7 +491,9 @@ int nvfp4_kv_append(const nvfp4_kv_cache_t* cache, const void* k, int64_t k_toke
  * and zeros where it sees none.  Tokens that it does not see have no effect,
  * NaN codes among them included.  Products and sums are in 32 bits; weights
  * are rounded to the 2-byte dtype for their product with the values (float32:
- * to three bf16 parts, exactly).
+ * to three bf16 parts, exactly).  With f16 a weight times its page's value
+ * scale that is below 2^-25 of the row's largest one is off by at most 2^-36
+ * of that.
  *
  * workspace (device, 16-byte aligned, of at least
  * nvfp4_paged_attention_workspace_size bytes) holds the partial results of a

@@ -14,8 +14,8 @@
 // Scales.  Keys: the score of a token is multiplied by its page's power of
 // two.  Values: with s the score in powers of two and e the exponent of the
 // value scale, the weight in units of codes is 2^(s + e), so the running
-// maximum m is that of s + e, the weights 2^(s + e - m) are at most 1 in any
-// type, and the sum of the softmax takes each of them times 2^-e.
+// maximum m is that of s + e, weights are 2^(s + e - r) against a reference r
+// that follows m, and the sum of the softmax takes each of them times 2^-e.
 //
 // What a row does not see gets s = -inf.  A NaN code among its values would
 // still spoil the product, as 0 * NaN: a tile that is not seen whole by all
@@ -73,6 +73,44 @@ struct Mma<_Float16> {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
   }
 };
+
+// The range of weights.  In bf16 and float32 they reach 1 or a little more.  f16
+// has its 11 bits down to 2^-14 only and nothing below 2^-25: there r lies below
+// m, weights reach 2^15, and one of 2^-25 of the largest still has all its bits;
+// a smaller one is off by at most 2^-36 of the largest.  (With weights up to 1
+// a row of 20000 tokens beside one of 17 nats more lost them all.)
+//
+// The exponent of a value scale counts within [kLeast, kLast]: 2^-e has to stay
+// in 32 bits, and the weights take the rest.  In f16 they could not take more
+// than 1 (and the sum does without: the largest weight is above 2^11).
+template <typename T>
+struct Range {
+  static constexpr float kSetFew = 0.0f, kSetMany = 0.0f, kMostMany = 8.0f, kLeast = -60.0f, kLast = 60.0f;
+};
+template <>
+struct Range<_Float16> {
+  static constexpr float kSetFew = 15.0f, kSetMany = 11.0f, kMostMany = 15.0f, kLeast = -60.0f, kLast = 128.0f;
+};
+// kSet: the exponent of the largest weight when the reference is set, kMostMany
+// that at which the many-rows kernel raises it.  Where scores are rounded by
+// more than the room to f16's largest number, the reference is the maximum.
+template <typename T>
+__device__ __forceinline__ float room(float exponent, bool huge) {
+  return __is_same(T, _Float16) && huge ? 0.0f : exponent;
+}
+
+struct ValueScale {
+  float e, rest, back;   // what counts of the exponent, the factor of the weights, 2^-e
+};
+template <typename T>
+__device__ __forceinline__ ValueScale value_scale(int byte) {
+  const float all = (float)(byte - 127);
+  ValueScale r;
+  r.e = all < Range<T>::kLeast ? Range<T>::kLeast : all > Range<T>::kLast ? Range<T>::kLast : all;
+  r.rest = __builtin_ldexpf(1.0f, (int)(all - r.e));
+  r.back = __builtin_ldexpf(1.0f, -(int)r.e);
+  return r;
+}
 
 // Eight codes (two words) as an operand, exactly.
 template <typename V8>
@@ -275,7 +313,7 @@ __global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>:
 
   constexpr int STEP = 64 * kFewWaves;
   uint4 kreg[4][U], vreg[CB];
-  float kscale = 0.0f, vexp = 0.0f;
+  float kscale = 0.0f;
   int kbyte = 0, vbyte = 0;
 
   // Key rows of lane n come from token group n / 4, values from group g.
@@ -317,7 +355,7 @@ __global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>:
     entry_k = entry_of(t_next + STEP + tk);
     entry_v = entry_of(t_next + STEP + tv);
     kscale = __builtin_ldexpf(A.scale_log2, kbyte - 127);
-    vexp = (float)(vbyte - 127);
+    const ValueScale vs = value_scale<T>(vbyte);
 
     // S^T
     f32x4_t sc[NT][4];
@@ -347,8 +385,6 @@ __global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>:
     // what each row sees; a tile that all rows see whole needs no comparison
     const bool whole = t0 + 63 <= sp.first && (A.window <= 0 || t0 > sp.last - A.window) && t0 + 64 <= hi &&
                        __all(idv >= 0);   // columns without a row may hold anything
-    float e = vexp < -60.0f ? -60.0f : vexp > 60.0f ? 60.0f : vexp;
-    const float rest = pow2(vexp - e), back = pow2(-e);
     V8 pw[NT][2][PARTS];
     uint32_t seen[NT];
 #pragma unroll
@@ -368,7 +404,7 @@ __global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>:
       // a lane's tokens share their scales: of a tile that is seen whole only
       // the largest score is scaled for the maximum (the factor is not
       // negative).  Float32 leaves no registers for both ways.
-      float w[16], top, mul = kscale, add = e;
+      float w[16], top, mul = kscale, add = vs.e;
       bool scaled = PARTS > 1 || !whole;
       if (PARTS == 1 && whole) {
         top = sc[nt][0][0];
@@ -381,14 +417,15 @@ __global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>:
         top = -__builtin_inff();
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float x = (seen[nt] >> i) & 1 ? __builtin_fmaf(sc[nt][i / 4][i % 4], kscale, e) : -__builtin_inff();
+          const float x = (seen[nt] >> i) & 1 ? __builtin_fmaf(sc[nt][i / 4][i % 4], kscale, vs.e) : -__builtin_inff();
           sc[nt][i / 4][i % 4] = x;
           top = fmaxf(top, x);
         }
         mul = 1.0f;
         add = 0.0f;
       }
-      const float m_new = fmaxf(m[nt], max_across_groups(top));
+      top = max_across_groups(top);
+      const float m_new = fmaxf(m[nt], top - room<T>(Range<T>::kSetFew, huge_score(top)));
       const float base = m_new == -__builtin_inff() ? 0.0f : m_new;
       const float alpha = pow2(m[nt] - base), less = add - base;
       m[nt] = m_new;
@@ -398,14 +435,14 @@ __global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>:
         w[i] = pow2(__builtin_fmaf(sc[nt][i / 4][i % 4], mul, less));
         sum += w[i];
       }
-      l[nt] = __builtin_fmaf(sum, back, l[nt] * alpha);
+      l[nt] = __builtin_fmaf(sum, vs.back, l[nt] * alpha);
 #pragma unroll
       for (int c = 0; c < CB; ++c) o[nt][c] *= alpha;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         float x[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = w[8 * s + i] * rest;
+        for (int i = 0; i < 8; ++i) x[i] = w[8 * s + i] * vs.rest;
         to_parts<T>(x, pw[nt][s]);
       }
     }
@@ -558,9 +595,8 @@ __global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>:
 // them.  Rows of LDS are stored with their 16-byte pieces permuted by the row
 // number, so that lanes reading down a column of pieces meet all banks.
 //
-// The running maximum is raised only once a score passes it by 2^8: a weight
-// of 256 is as exact in every type as one of 1, and most tiles leave the sums
-// alone.
+// The reference is raised only once a score passes it by kMostMany: most tiles
+// leave the sums alone.
 //
 // Bound by the vector units beside the matrix cores: a wave's tile is 32
 // exponentials, 16 maxima, 32 scalings, 32 sums and 16 conversions a lane
@@ -588,7 +624,8 @@ struct Mma32<_Float16> {
 
 // What the four groups of 16 tokens of a tile have in common.
 struct GroupInfo {
-  float kscale, e, rest, back;   // score factor; clamped exponent of the values, what the clamp left, 2^-e
+  float kscale;                  // score factor
+  float e, rest, back;           // of ValueScale
 };
 
 // Where the pieces of 16 bytes of row r lie: 16 lanes read a column of pieces
@@ -608,7 +645,7 @@ struct ManyShared {
   ManyTile<DIM> tile[2];
   GroupInfo info[2][4];
   uint32_t there[2];   // bit g: group g's page is there
-  uint32_t clamped[2]; // some group's rest is not 1
+  uint32_t far[2];     // some group's rest is not 1
   int32_t nan[2];      // the first token of the last partial tile here that had a NaN code among its values,
   __align__(8) uint16_t nan_tokens[2][DIM][4];   // and which ones: a bit per token
 };
@@ -763,20 +800,13 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1
       t.v[c * 8 + ((2 * vg) ^ swizzle<8>(c))] = __builtin_bit_cast(uint4, decode8<V8>(vreg[i].x, vreg[i].y));
       t.v[c * 8 + ((2 * vg + 1) ^ swizzle<8>(c))] = __builtin_bit_cast(uint4, decode8<V8>(vreg[i].z, vreg[i].w));
     }
-    if (tid < 4) {
-      GroupInfo f;
-      const float e = (float)(vbyte - 127);
-      f.kscale = __builtin_ldexpf(A.scale_log2, kbyte - 127);
-      f.e = e < -60.0f ? -60.0f : e > 60.0f ? 60.0f : e;
-      f.rest = pow2(e - f.e);
-      f.back = pow2(-f.e);
-      S.info[at][tid] = f;
-    }
     if (wave == 0) {
-      const uint64_t there = __ballot(id[VALUES] >= 0), far = __ballot(vbyte < 67 || vbyte > 187);
+      const ValueScale vs = value_scale<T>(vbyte);
+      if (tid < 4) S.info[at][tid] = {__builtin_ldexpf(A.scale_log2, kbyte - 127), vs.e, vs.rest, vs.back};
+      const uint64_t there = __ballot(id[VALUES] >= 0), far = __ballot(vs.rest != 1.0f);
       if (tid == 0) {
         S.there[at] = (uint32_t)there & 0xfu;
-        S.clamped[at] = (uint32_t)far & 0xfu;
+        S.far[at] = (uint32_t)far & 0xfu;
       }
     }
   };
@@ -870,8 +900,9 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1
         }
       }
       top = fmaxf(top, __shfl_xor(top, 32, 64));
-      if (__any(top > m + 8.0f)) {
-        const float m_new = fmaxf(m, top);
+      const bool huge = huge_score(top);
+      if (__any(top > m + room<T>(Range<T>::kMostMany, huge))) {
+        const float m_new = fmaxf(m, top - room<T>(Range<T>::kSetMany, huge));
         const float alpha = pow2(m - (m_new == -__builtin_inff() ? 0.0f : m_new));
         m = m_new;
         l *= alpha;
@@ -892,7 +923,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1
         }
         l = __builtin_fmaf(sum, back, l);
       }
-      if (S.clamped[at]) {   // value scales outside 2^-60 .. 2^60
+      if (S.far[at]) {
 #pragma unroll
         for (int g = 0; g < 4; ++g)
 #pragma unroll

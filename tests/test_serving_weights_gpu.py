@@ -1,5 +1,10 @@
-"""Attention's weights at the ends of their range.  Tolerances are those of
-test_serving_gpu.py unless a test says otherwise."""
+"""Attention's weights at the ends of their range.
+
+Tolerances are those of test_serving_gpu.py, and of f16 weights one more: in
+units of the values' codes, weights below 2^-25 of the largest are off by at
+most 2^-36 of that one."""
+
+import math
 
 import math
 
@@ -37,6 +42,35 @@ def attention(q, cache, table, n, scale):
     return got.double().cpu()
 
 
+def check(q, cache, table, n, scale):
+    """Against 64 bits; returns the exact output."""
+    got = attention(q, cache, table, n, scale)
+    k, v, ks, vs = cache
+    page, dim = k.shape[2:]
+    ids, h = table[0].long(), torch.finfo(q.dtype).eps / 2
+    at, t = torch.arange(n - q.shape[0], n), torch.arange(n)
+    kk = (E4M3[k[ids, 0].long()] * torch.exp2(ks[ids, 0].double() - 127)[:, None, None]).reshape(-1, dim)[:n]
+    codes = E4M3[v[ids, 0].long()].transpose(1, 2).reshape(-1, dim)[:n]
+    scales = torch.exp2(vs[ids, 0].double() - 127).repeat_interleave(page)[:n]
+    scale = float(np.float32(scale))
+    for j in range(q.shape[1]):
+        x = q[:, j].double()
+        s = torch.where(t <= at[:, None], x @ kk.T * scale, -math.inf)
+        size = (x.abs() @ kk.abs().T * scale).amax(1, keepdim=True)
+        units = torch.softmax(s, 1) * scales
+        ref, amount = units @ codes, units @ codes.abs()
+        rel = 2.0 ** -24 * (2 * ((dim + 8) * size + 6 * size + 16) + n + 16)
+        tol = h * ref.abs() + rel * amount + torch.finfo(q.dtype).smallest_normal * h
+        if q.dtype != F32:
+            tol = tol + h * (1 + h) * amount
+        if q.dtype == F16:
+            tol = tol + 2.0 ** -36 * units.amax(1, keepdim=True) * codes.abs().sum(0)
+        assert got[:, j].isfinite().all()
+        err = (got[:, j] - ref).abs() - tol
+        assert err.max() <= 0, (j, float(err.max()), float((got[:, j] - ref).abs().max()), float(ref.abs().max()))
+    return ref
+
+
 # 1 and 40 new tokens: few rows and many
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
 @pytest.mark.parametrize("count", [1, 40])
@@ -61,3 +95,70 @@ def test_scores_of_any_size(dtype, count, power):
         tol = h * (a + b).abs() / 2 + (weights * (1 + h) + 2.0 ** -20) * (a.abs() + b.abs()) / 2
         assert ((got - (a + b) / 2).abs() <= tol).all()
         assert attention(-q, cache, table, n, 2.0 ** power).isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("count", [1, 40])
+@pytest.mark.parametrize("code,nats", [(0x58, 14.0), (0x58, 17.5), (0x58, 20.0)])
+def test_many_small_weights_beside_a_large_one(dtype, count, code, nats):
+    """One token of zeros `nats` above 20000 others: the output is the others'."""
+    n = 20000
+    q, cache, table = state(2, dtype, n, count)
+    one_hot(q, cache)
+    first = int(table[0, 0])
+    cache[0][first, 0, 0, 0] = code                       # 16
+    cache[1][first, 0, :, 0] = 0
+    assert check(q, cache, table, n, nats / 16).abs().max() > 1e-7
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("count", [1, 40])
+@pytest.mark.parametrize("exponent", [8, 20, 26])
+def test_a_page_with_a_value_scale_far_above_the_others(dtype, count, exponent):
+    """Equal weights; the loud page is loud in one channel only, the others are not lost."""
+    n = 1000
+    q, cache, table = state(3, dtype, n, count)
+    one_hot(q, cache)
+    v, vs = cache[1], cache[3]
+    loud = int(table[0, 1])
+    vs[loud] = 127 + exponent
+    v[loud] = 0
+    v[loud, 0, 5] = 0x01                                  # 2^-9
+    check(q, cache, table, n, 1.0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("count", [1, 40])
+@pytest.mark.parametrize("exponent", [-110, -61, -60, 60, 61, 100])
+def test_value_scales_at_the_ends(dtype, count, exponent):
+    """All pages at the scale, and one of zeros whose byte is 0."""
+    n = 300
+    q, cache, table = state(4, dtype, n, count)
+    cache[3].fill_(127 + exponent)
+    zeros = int(table[0, 2])
+    cache[1][zeros], cache[3][zeros] = 0, 0
+    check(q, cache, table, n, 0.125)
+
+
+@pytest.mark.parametrize("count", [1, 40])
+@pytest.mark.parametrize("exponent", [16, 60, 61, 76, 100, 128])
+def test_f16_zeros_at_a_scale_past_f16(count, exponent):
+    """A float32 model's page may have such a scale; its zeros are no NaN."""
+    q, cache, table = state(5, F16, 300, count)
+    one_hot(q, cache)
+    loud = int(table[0, 1])
+    cache[1][loud], cache[3][loud] = 0, 127 + exponent
+    check(q, cache, table, 300, 1.0)
+
+
+@pytest.mark.parametrize("count", [1, 40])
+def test_f16_scores_that_grow_along_the_row(count):
+    """Each tile's largest score passes the one before, by less and by more
+    than the reference waits for."""
+    n = 640
+    for step in (1.0, 4.0, 9.0, 12.0):
+        q, cache, table = state(7, F16, n, count)
+        one_hot(q, cache)
+        for i, page in enumerate(table[0]):
+            cache[0][int(page), 0, :, 0] = torch.tensor([0, 0x38, 0x40, 0x44, 0x48, 0x4a, 0x4c, 0x4e, 0x50, 0x51])[i]
+        check(q, cache, table, n, step)
