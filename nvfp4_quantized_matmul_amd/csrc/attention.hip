@@ -206,7 +206,8 @@ __device__ __forceinline__ Span span_of(const AttnArgs& A, const Sequence& s, in
   const int64_t cap = A.s.width << A.c.page_shift;
   r.end = r.last + 1 < cap ? r.last + 1 : (int32_t)cap;
   const int32_t lo = A.window > 0 && r.first >= A.window ? r.first - A.window + 1 : 0;
-  r.begin = lo & ~63;
+  // behind the table there is nothing, and positions from there on would pass 32 bits
+  r.begin = (lo < cap ? lo : (int32_t)cap) & ~63;
   return r;
 }
 
