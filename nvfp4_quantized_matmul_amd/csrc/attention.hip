@@ -199,13 +199,18 @@ struct Span {
   int32_t begin, end;    // cached tokens that any of the rows sees; begin on a tile
 };
 
+// The first position that a row at position p sees through the window.
+__device__ __forceinline__ int32_t first_seen(const AttnArgs& A, int32_t p) {
+  return A.window > 0 && p >= A.window ? p - A.window + 1 : 0;
+}
+
 __device__ __forceinline__ Span span_of(const AttnArgs& A, const Sequence& s, int t0, int t1) {
   Span r;
   r.first = s.len - s.count + t0;
   r.last = s.len - s.count + t1;
   const int64_t cap = A.s.width << A.c.page_shift;
   r.end = r.last + 1 < cap ? r.last + 1 : (int32_t)cap;
-  const int32_t lo = A.window > 0 && r.first >= A.window ? r.first - A.window + 1 : 0;
+  const int32_t lo = first_seen(A, r.first);
   // behind the table there is nothing, and positions from there on would pass 32 bits
   r.begin = (lo < cap ? lo : (int32_t)cap) & ~63;
   return r;
@@ -301,6 +306,7 @@ __global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>:
     for (int c = 0; c < CB; ++c) o[nt][c] = f32x4_t{0, 0, 0, 0};
   }
 
+  const int from_last = first_seen(A, sp.last);
   const int shift = A.c.page_shift, pmask = (1 << shift) - 1;
   const int32_t* table = A.s.table + (int64_t)b * A.s.width;
   const int64_t page_bytes = (int64_t)DIM << shift;
@@ -384,7 +390,7 @@ __global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>:
     load_k(t_load, idk_next);
 
     // what each row sees; a tile that all rows see whole needs no comparison
-    const bool whole = t0 + 63 <= sp.first && (A.window <= 0 || t0 > sp.last - A.window) && t0 + 64 <= hi &&
+    const bool whole = t0 + 63 <= sp.first && t0 >= from_last && t0 + 64 <= hi &&
                        __all(idv >= 0);   // columns without a row may hold anything
     V8 pw[NT][2][PARTS];
     uint32_t seen[NT];
@@ -396,7 +402,7 @@ __global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>:
         const int tg = t0 + 16 * g;
         // tokens tg + i with i <= last_i and i >= first_i
         const int last_i = (pos[nt] < hi ? pos[nt] : hi - 1) - tg;
-        const int first_i = A.window > 0 ? pos[nt] - A.window + 1 - tg : 0;
+        const int first_i = first_seen(A, pos[nt]) - tg;
         if (idv >= 0) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) seen[nt] |= (i <= last_i && i >= first_i) ? 1u << i : 0u;
@@ -686,7 +692,8 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1
   const int lo = (int)lo64;
   const int hi = sp.end - lo < A.chunk ? sp.end : lo + A.chunk;
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 31, hh = lane >> 5;
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, hh = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);   // what goes by the wave stays in scalar registers
   const int shift = A.c.page_shift, pmask = (1 << shift) - 1;
   const int32_t* table = A.s.table + (int64_t)b * A.s.width;
   const int64_t page_bytes = (int64_t)DIM << shift;
@@ -710,6 +717,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1
   const int wave_rows = nrows - wave * 32 < 32 ? nrows - wave * 32 : 32;
   const int wfirst = wave_rows > 0 ? base_pos + (row0 + wave * 32) / A.group : 0;
   const int wlast = wave_rows > 0 ? base_pos + (row0 + wave * 32 + wave_rows - 1) / A.group : -1;
+  const int from_wfirst = first_seen(A, wfirst), from_wlast = first_seen(A, wlast), from_last = first_seen(A, sp.last);
 
   auto page_of = [&](int t) -> int {
     if (t >= hi) return -1;
@@ -821,7 +829,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1
 
   // a tile is partial for the block if a row does not see it whole or a page is missing
   auto partial = [&](int t0) -> bool {
-    return t0 + 63 > sp.first || (A.window > 0 && t0 <= sp.last - A.window) || t0 + 64 > hi || __any(id[VALUES] < 0);
+    return t0 + 63 > sp.first || t0 < from_last || t0 + 64 > hi || __any(id[VALUES] < 0);
   };
 
   if (tid < 2) S.nan[tid] = -1;
@@ -841,7 +849,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1
     load(t0 + 64);   // also behind the last tile, from page 0
     const bool next_partial = partial(t0 + 64);
     const ManyTile<DIM>& t = S.tile[at];
-    const bool unseen = t0 > wlast || (A.window > 0 && t0 + 63 <= wfirst - A.window);
+    const bool unseen = t0 > wlast || t0 + 63 < from_wfirst;
     if (!unseen) {
       f32x16_t sc[2];
 #pragma unroll
@@ -857,7 +865,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1
         }
       }
       const uint32_t there = S.there[at];
-      const bool whole = t0 + 63 <= wfirst && (A.window <= 0 || t0 > wlast - A.window) && wave_rows == 32 && there == 0xfu;
+      const bool whole = t0 + 63 <= wfirst && t0 >= from_wlast && wave_rows == 32 && there == 0xfu;
       // the largest score, and the factor and summand that make weights of
       // scores: of tiles that are seen whole only the largest of each group of
       // 16 tokens is scaled for it (the factors are not negative)
@@ -881,7 +889,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1
       }
       if (scaled) {
         top = -__builtin_inff();
-        const int last_i = pos - t0, first_i = A.window > 0 ? pos - A.window + 1 - t0 : 0;
+        const int last_i = pos - t0, first_i = first_seen(A, pos) - t0;
         vis = last_i < 0 ? 0 : last_i >= 63 ? ~0ull : (2ull << last_i) - 1;
         if (first_i > 0) vis = first_i > 63 ? 0 : vis & (~0ull << first_i);
 #pragma unroll
@@ -1184,7 +1192,8 @@ void launch_paged_attention(const nvfp4_kv_cache_t& c, const void* q, int64_t q_
   A.part_m = p.splits > 1 ? A.part_o + prow * c.dim : nullptr;
   A.part_l = p.splits > 1 ? A.part_m + prow : nullptr;
   A.heads_q = (int32_t)heads_q; A.group = (int32_t)(heads_q / c.heads);
-  A.window = window <= 0 || window >= width * c.page ? 0 : (int32_t)window;   // a window over the whole table is none
+  // none where it passes all positions; lengths may pass the table, so its size says nothing
+  A.window = window <= 0 || window > INT_MAX ? 0 : (int32_t)window;
   A.splits = (int32_t)p.splits; A.chunk = (int32_t)p.chunk;
   A.row_tiles = (int32_t)p.row_tiles;
   A.sign = scale < 0.0f ? -1.0f : 1.0f;

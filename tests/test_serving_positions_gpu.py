@@ -79,3 +79,17 @@ def test_lengths_at_the_end_of_int32(dtype, count, window):
 def test_lengths_at_the_end_of_int32_over_a_split_axis(dtype):
     got = run(2, dtype, 4, 1, 64, 64, 100, [END, END - 100], [1, 1], 5000)
     assert (got == 0).all()
+
+
+@pytest.mark.parametrize("dtype,hq,count", [(BF16, 4, 1), (F16, 2, 40), (F32, 2, 5)])
+@pytest.mark.parametrize("window", [1, 100, 127, 128, 129, 150, 200, 2 ** 31 - 1, 2 ** 31, 2 ** 40])
+def test_windows_around_the_table(dtype, hq, count, window):
+    """A table of 128 tokens; lengths inside it, a little past it, and past it
+    by as much as the windows and more."""
+    run(3, dtype, hq, 1, 64, 32, 4, [100, 128, 129, 170, 228, 327, 400], [count] * 7, window)
+
+
+@pytest.mark.parametrize("dtype,hq,count", [(BF16, 4, 1), (F16, 4, 40), (F32, 2, 3)])
+@pytest.mark.parametrize("window", [3000, 6400, 6500])
+def test_windows_around_a_split_table(dtype, hq, count, window):
+    run(4, dtype, hq, 1, 64, 64, 100, [6300, 7000, 9500, 13000], [count] * 4, window)
