@@ -427,9 +427,9 @@ int64_t nvfp4_qmv_max_rows(void);
  * one after the other in rows [cu_q[b], cu_q[b + 1]) of q, k and v, with
  * cu_q int32 [batch + 1] from 0 to `tokens`; with cu_q NULL every sequence
  * has one new token and tokens == batch.  max_q is an upper bound of the new
- * tokens of a sequence that sizes the launch; it does not change a result
- * (new tokens past a bound that is too small are left out, their rows of the
- * outputs unwritten).
+ * tokens of a sequence that sizes the launch; it does not change a result.
+ * Of a sequence with more the calls take the first max_q, at their positions:
+ * the others are not cached and their rows of the outputs not written.
  * Tensors of tokens are [tokens, heads, dim] with the last axis contiguous
  * and any strides (in elements, >= 0) of the other two.
  *

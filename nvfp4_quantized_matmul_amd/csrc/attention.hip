@@ -206,8 +206,8 @@ __device__ __forceinline__ int32_t first_seen(const AttnArgs& A, int32_t p) {
 
 __device__ __forceinline__ Span span_of(const AttnArgs& A, const Sequence& s, int t0, int t1) {
   Span r;
-  r.first = s.len - s.count + t0;
-  r.last = s.len - s.count + t1;
+  r.first = s.first + t0;
+  r.last = s.first + t1;
   const int64_t cap = A.s.width << A.c.page_shift;
   r.end = r.last + 1 < cap ? r.last + 1 : (int32_t)cap;
   const int32_t lo = first_seen(A, r.first);
@@ -699,7 +699,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1
   const int64_t page_bytes = (int64_t)DIM << shift;
 
   // the wave's queries, in registers: step s holds channels 16 s + 8 hh .. + 7
-  const int my = wave * 32 + n, base_pos = sq.len - sq.count;
+  const int my = wave * 32 + n, base_pos = sq.first;
   const int pos = my < nrows ? base_pos + (row0 + my) / A.group : -1;
   V8 q[KS];
   {
@@ -1183,7 +1183,7 @@ void launch_paged_attention(const nvfp4_kv_cache_t& c, const void* q, int64_t q_
   if (ws_bytes < partials(p, tokens, heads_q, c.dim)) p = make_plan(heads_q, c.heads, c.page, batch, max_q, width, window, dt, c.dim, false);
   AttnArgs A;
   A.c = {c.k, c.v, c.k_scales, c.v_scales, (int32_t)c.pages, (int32_t)c.heads, __builtin_ctz((unsigned)c.page)};
-  A.s = {table, lens, cu, width, (int32_t)batch, (int32_t)tokens};
+  A.s = {table, lens, cu, width, (int32_t)batch, (int32_t)tokens, (int32_t)max_q};
   A.q = q; A.q_token = q_token; A.q_head = q_head;
   A.out = out;
   if (c.pages == 0) A.s.width = 0;   // no page to read: nothing is seen

@@ -345,6 +345,9 @@ __device__ void append_values(const AppendArgs& A, const T* v, uint8_t* codes, u
   if (threadIdx.x == 0) *scale = (uint8_t)byte;
 }
 
+// In place of a position (of a row past the tokens that the call takes).
+constexpr int kLeftOut = INT_MIN;
+
 template <typename T, int W, bool INTER>
 __device__ void rotate_queries(const AppendArgs& A, int64_t block, double2* turn, int* pos) {
   // turn [q_tokens][rot / 2]: (sin, cos); pos [q_tokens]
@@ -365,11 +368,15 @@ __device__ void rotate_queries(const AppendArgs& A, int64_t block, double2* turn
     int p = 0;   // rows of no sequence are copied unturned
     if (b < A.s.batch) {
       const Sequence s = sequence(A.s, b);
-      p = s.len - s.count + (t - s.row0);
+      p = t - s.row0 < s.count ? s.first + (t - s.row0) : kLeftOut;
     }
     pos[threadIdx.x] = p;
   }
   __syncthreads();
+  uint32_t left_out = 0;   // a bit per row
+#pragma unroll
+  for (int t = 0; t < kTokensWide; ++t) left_out |= t < n && pos[t] == kLeftOut ? 1u << t : 0u;
+  left_out = __builtin_amdgcn_readfirstlane(left_out);
   const int half = A.rot / 2;
   for (int i = threadIdx.x; i < n * half; i += kThreads) {
     const int t = i / half, f = i - t * half;
@@ -380,40 +387,48 @@ __device__ void rotate_queries(const AppendArgs& A, int64_t block, double2* turn
   }
   __syncthreads();
   const int per = A.dim / (2 * W), turning = A.rot / (2 * W), row_items = A.heads_q * per;
-  // the loads of several items in flight at a time
-  const int all = n * row_items;
-  for (int it0 = threadIdx.x; it0 < all; it0 += kQueryItems * kThreads) {
-    float a[kQueryItems][W], b[kQueryItems][W];
+  // rows [ta, tb), the loads of several items in flight at a time
+  const auto rows = [&](int ta, int tb) {
+    const int all = tb * row_items;
+    for (int it0 = ta * row_items + threadIdx.x; it0 < all; it0 += kQueryItems * kThreads) {
+      float a[kQueryItems][W], b[kQueryItems][W];
 #pragma unroll
-    for (int r = 0; r < kQueryItems; ++r) {
-      const int it = it0 + r * kThreads;
-      if (it < all) {
-        const int t = it / row_items, rest = it - t * row_items, h = rest / per;
-        int ca, cb;
-        item_channels<W, INTER>(rest - h * per, A.rot, &ca, &cb);
-        const T* row = (const T*)A.q + (int64_t)(t0 + t) * A.q_token + (int64_t)h * A.q_head;
-        load_group<T, W>(row + ca, a[r]);
-        load_group<T, W>(row + cb, b[r]);
+      for (int r = 0; r < kQueryItems; ++r) {
+        const int it = it0 + r * kThreads;
+        if (it < all) {
+          const int t = it / row_items, rest = it - t * row_items, h = rest / per;
+          int ca, cb;
+          item_channels<W, INTER>(rest - h * per, A.rot, &ca, &cb);
+          const T* row = (const T*)A.q + (int64_t)(t0 + t) * A.q_token + (int64_t)h * A.q_head;
+          load_group<T, W>(row + ca, a[r]);
+          load_group<T, W>(row + cb, b[r]);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < kQueryItems; ++r) {
+        const int it = it0 + r * kThreads;
+        if (it < all) {
+          const int t = it / row_items, rest = it - t * row_items, h = rest / per, j = rest - h * per;
+          int ca, cb;
+          item_channels<W, INTER>(j, A.rot, &ca, &cb);
+          if (j < turning)
+            rotate_item<W, INTER>(a[r], b[r], [&](int i, double* sn, double* cs) {
+              const double2 d = turn[t * half + W * j + i];
+              *sn = d.x;
+              *cs = d.y;
+            });
+          T* out = (T*)A.q_out + ((int64_t)(t0 + t) * A.heads_q + h) * A.dim;
+          store_group<T, W>(out + ca, a[r]);
+          store_group<T, W>(out + cb, b[r]);
+        }
       }
     }
-#pragma unroll
-    for (int r = 0; r < kQueryItems; ++r) {
-      const int it = it0 + r * kThreads;
-      if (it < all) {
-        const int t = it / row_items, rest = it - t * row_items, h = rest / per, j = rest - h * per;
-        int ca, cb;
-        item_channels<W, INTER>(j, A.rot, &ca, &cb);
-        if (j < turning)
-          rotate_item<W, INTER>(a[r], b[r], [&](int i, double* sn, double* cs) {
-            const double2 d = turn[t * half + W * j + i];
-            *sn = d.x;
-            *cs = d.y;
-          });
-        T* out = (T*)A.q_out + ((int64_t)(t0 + t) * A.heads_q + h) * A.dim;
-        store_group<T, W>(out + ca, a[r]);
-        store_group<T, W>(out + cb, b[r]);
-      }
-    }
+  };
+  if (!left_out) {
+    rows(0, n);
+  } else {
+    for (int t = 0; t < n; ++t)
+      if (!((left_out >> t) & 1)) rows(t, t + 1);
   }
 }
 
@@ -432,14 +447,13 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs A) {
   block /= A.c.heads;
   const int slot = (int)(block % A.slots), b = (int)(block / A.slots);
   const Sequence s = sequence(A.s, b);
-  const int first = s.len - s.count;     // position of the sequence's first new token
-  const int from = first < 0 ? 0 : first;
+  const int first = s.first, stop = s.first + s.count, from = first < 0 ? 0 : first;
   const int64_t pi = (int64_t)(from >> A.c.page_shift) + slot;
   const int64_t page0 = pi << A.c.page_shift;
-  if (s.len <= 0 || pi >= A.s.width || page0 >= s.len) return;
+  if (pi >= A.s.width || page0 >= stop) return;
   const int pos0 = (int)page0, page = 1 << A.c.page_shift;
   const int begin = from > pos0 ? from : pos0;
-  const int end = s.len - pos0 < page ? s.len : pos0 + page;
+  const int end = stop - pos0 < page ? stop : pos0 + page;
   const int id = A.s.table[(int64_t)b * A.s.width + pi];
   if (begin >= end || id < 0 || id >= A.c.pages) return;
   const int64_t ph = (int64_t)id * A.c.heads + h;
@@ -481,7 +495,7 @@ void launch_kv_append(const nvfp4_kv_cache_t& c, const void* k, int64_t k_token,
                       const float* inv_freq, int64_t rot, bool inter, hipStream_t s) {
   AppendArgs A;
   A.c = {c.k, c.v, c.k_scales, c.v_scales, (int32_t)c.pages, (int32_t)c.heads, __builtin_ctz((unsigned)c.page)};
-  A.s = {table, lens, cu, width, (int32_t)batch, (int32_t)tokens};
+  A.s = {table, lens, cu, width, (int32_t)batch, (int32_t)tokens, (int32_t)max_q};
   A.k = k; A.v = v; A.q = q;
   A.k_token = k_token; A.k_head = k_head; A.v_token = v_token; A.v_head = v_head; A.q_token = q_token; A.q_head = q_head;
   A.q_out = q_out;

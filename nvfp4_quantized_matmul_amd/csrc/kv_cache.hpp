@@ -22,23 +22,24 @@ struct SequenceView {
   const int32_t* cu;     // [batch + 1] or nullptr: one new token each
   int64_t width;
   int32_t batch, tokens;
+  int32_t most;          // new tokens of a sequence that the call takes
 };
 
 struct Sequence {
   int32_t row0, count;  // rows [row0, row0 + count) of q, k and v
-  int32_t len;          // cached tokens, the new ones among them; may pass the table
+  int32_t first;        // position of the first of them; lengths may pass the table
 };
 
-// Sequence b, its rows cut to the rows that exist.
+// Sequence b, its rows cut to the rows that exist and to those that the call takes.
 __device__ __forceinline__ Sequence sequence(const SequenceView& sv, int b) {
   Sequence s;
   int lo = sv.cu ? sv.cu[b] : b, hi = sv.cu ? sv.cu[b + 1] : b + 1;
-  s.len = sv.lens[b];
-  s.len = s.len < 0 ? 0 : s.len;
+  const int len = sv.lens[b];
   lo = lo < 0 ? 0 : lo > sv.tokens ? sv.tokens : lo;
   hi = hi < lo ? lo : hi > sv.tokens ? sv.tokens : hi;
   s.row0 = lo;
-  s.count = hi - lo;
+  s.first = (len < 0 ? 0 : len) - (hi - lo);
+  s.count = hi - lo < sv.most ? hi - lo : sv.most;
   return s;
 }
 

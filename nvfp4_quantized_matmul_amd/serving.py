@@ -150,7 +150,8 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, table: torch.Ten
     pages of each sequence, in order; lens int32 [batch]: its tokens, the new
     ones among them; cu_q int32 [batch + 1]: the rows of its new tokens
     (default: one each); max_q: an upper bound of a sequence's new tokens
-    (default: all of them) that sizes the launch, tokens past it are left out.
+    (default: all of them) that sizes the launch; a sequence's tokens past it
+    are left out, and their rows of the result not written.
 
     inv_freq float32 [rot / 2]: channels [0, rot) of keys and queries turn by
     position * inv_freq[i], in the pairs (i, i + rot / 2) or, interleaved,
