@@ -513,7 +513,8 @@ int nvfp4_paged_attention(const nvfp4_kv_cache_t* cache, const void* q, int64_t 
  *
  *   logits       [batch, vocab] of dtype, row stride row_stride (elements)
  *   u            float [batch], in [0, 1)
- *   temperature  float [batch] or NULL (1)
+ *   temperature  float [batch] or NULL (1); one that is not above 0 leaves the
+ *                largest logits alone, with equal weights
  *   top_k        int32 [batch] or NULL; <= 0 keeps all
  *   top_p, min_p float [batch] or NULL; 1 and 0 keep all
  *   token        int32 [batch]

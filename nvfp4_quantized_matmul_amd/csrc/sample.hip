@@ -88,6 +88,13 @@ __device__ __forceinline__ double exp2_64(double y) {
 // instructions that run once, so what is off the loops is kept small.
 __device__ __noinline__ double exp2_call(double y) { return exp2_64(y); }
 
+// log2(e) / temperature, never negative: weights are at most 1, and their sums
+// in 62 bits do not wrap.
+__device__ __forceinline__ double rate_of(const SampleArgs& A, int row) {
+  const double t = A.temperature ? (double)A.temperature[row] : 1.0;
+  return t > 0.0 ? 1.44269504088896340736 / t : __builtin_inf();
+}
+
 // exp((x - top) / temperature), with rate = log2(e) / temperature.
 __device__ __forceinline__ double weight(float x, float top, double rate) {
   if (x == top) return 1.0;
@@ -117,9 +124,10 @@ __device__ __forceinline__ V wave_inclusive(V v) {
 }
 
 // The bin, from the top down, in which the sum before it is still below
-// `target` and the sum with it is not (the last non-empty one if rounding
-// leaves none): into S.bin, the sum before it into S.before.  `value` gives a
-// bin's amount; bins 2 t and 2 t + 1 from the top are thread t's.
+// `target` and the sum with it is not: into S.bin, the sum before it into
+// S.before.  There is one, as before0 is below the target and the whole is not,
+// and conversions to double keep the order.  `value` gives a bin's amount; bins
+// 2 t and 2 t + 1 from the top are thread t's.
 template <typename F>
 __device__ void find_bin(Shared& S, double target, const F& value, unsigned long long before0) {
   static_assert(kBins == 2 * kThreads, "two bins a thread");
@@ -128,7 +136,6 @@ __device__ void find_bin(Shared& S, double target, const F& value, unsigned long
   const unsigned long long v0 = value(b0), v1 = value(b1);
   const unsigned long long incl = wave_inclusive<unsigned long long>(v0 + v1);
   if (lane == 63) S.wave_mass[wave] = incl;
-  if (tid == 0) S.bin = 0xffffffffu;
   __syncthreads();
   unsigned long long before = before0;
   for (int w = 0; w < wave; ++w) before += S.wave_mass[w];
@@ -137,19 +144,6 @@ __device__ void find_bin(Shared& S, double target, const F& value, unsigned long
   const unsigned long long mid = before + v0;
   if (v1 && (double)mid < target && (double)(mid + v1) >= target) { S.bin = b1; S.before = mid; }
   __syncthreads();
-  if (S.bin == 0xffffffffu) {
-    // only where the target passes the whole by a rounding: the lowest non-empty bin
-    if (tid == 0) {
-      unsigned long long sum = before0;
-      for (int b = kBins - 1; b >= 0; --b) {
-        const unsigned long long v = value(b);
-        if (v) { S.bin = b; S.before = sum; }
-        sum += v;
-      }
-      if (S.bin == 0xffffffffu) { S.bin = 0; S.before = sum; }
-    }
-    __syncthreads();
-  }
 }
 
 // Narrows [lo, hi) to the first index whose running sum of f passes a target:
@@ -237,7 +231,7 @@ __device__ __noinline__ void row_by_digits(const SampleArgs& A, Shared& S, int r
     return;
   }
   auto at = [&](int i) -> float { return clean((float)x[i]); };
-  const double rate = 1.44269504088896340736 / (A.temperature ? (double)A.temperature[row] : 1.0);
+  const double rate = rate_of(A, row);
   int k = A.top_k ? A.top_k[row] : 0;
   double p = A.top_p ? (double)A.top_p[row] : 1.0;
   const double floor_w = A.min_p ? (double)A.min_p[row] : 0.0;
@@ -377,7 +371,7 @@ struct Settings {
 
 __device__ __forceinline__ Settings settings(const SampleArgs& A, int row) {
   Settings s;
-  s.rate = 1.44269504088896340736 / (A.temperature ? (double)A.temperature[row] : 1.0);
+  s.rate = rate_of(A, row);
   s.p = A.top_p ? (double)A.top_p[row] : 1.0;
   s.p = s.p == s.p ? s.p : 0.0;
   s.floor_w = A.min_p ? (double)A.min_p[row] : 0.0;
@@ -403,7 +397,7 @@ __device__ __forceinline__ Bins bins_of(float top, float least, double rate) {
   b.per_unit = range > 0.0 ? (kNB - 1) / range : 0.0;
   b.per_unit = b.per_unit < 1e100 ? b.per_unit : 1e100;
   b.unit = b.per_unit > 0.0 ? 1.0 / b.per_unit : 0.0;
-  b.digits = !(rate >= 0.0) || top == __builtin_inff();
+  b.digits = top == __builtin_inff();
   return b;
 }
 

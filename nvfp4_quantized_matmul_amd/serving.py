@@ -275,7 +275,8 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Te
     contiguous); u float32 [batch] in [0, 1); temperature, top_p, min_p
     float32 [batch] and top_k int32 [batch], or None for 1, 1, 0 and 0 (all
     kept).  Tokens are ordered by falling logit, equal ones by index; weights
-    are exp((logit - largest) / temperature).  top_k keeps the first k, top_p
+    are exp((logit - largest) / temperature), at a temperature that is not above
+    0 those of the largest alone.  top_k keeps the first k, top_p
     those of them with less than top_p of their sum before them, min_p those
     with at least min_p of the largest weight; the first one always stays.
     The token is the first kept one, by index, whose running sum of weights
