@@ -20,6 +20,7 @@
 // What a row does not see gets s = -inf.  A NaN code among its values would
 // still spoil the product, as 0 * NaN: a tile that is not seen whole by all
 // rows is searched for them, and one that holds any takes a separate path.
+#include <algorithm>
 #include <climits>
 
 #include "kv_cache.hpp"
@@ -1092,7 +1093,7 @@ Plan make_plan(int64_t heads_q, int64_t heads, int64_t page, int64_t batch, int6
     const int64_t w = window - 1 + (p.rows + group - 1) / group + 1 + 63;
     if (w < span) span = w;
   }
-  const int64_t tiles = (span + 63) / 64, base = batch * heads * p.row_tiles;
+  const int64_t tiles = (span + 63) / 64, base = batch * heads * p.row_tiles;   // max_q * heads_q is at most 2^30
   p.splits = 1;
   p.chunk = (tiles > 0 ? tiles : 1) * 64;
   if (split) {
@@ -1110,6 +1111,10 @@ Plan make_plan(int64_t heads_q, int64_t heads, int64_t page, int64_t batch, int6
   p.blocks = base * p.splits;
   return p;
 }
+
+// A wave a row joins up to kFewSplits splits, a block a row more of them.
+constexpr int64_t kFewSplits = 16;
+int64_t join_blocks(const Plan& p, int64_t rows) { return p.splits == 1 ? 0 : p.splits <= kFewSplits ? (rows + 3) / 4 : rows; }
 
 int64_t partials(const Plan& p, int64_t tokens, int64_t heads_q, int64_t dim) {
   return p.splits > 1 ? tokens * heads_q * p.splits * (dim + 2) * 4 : 0;
@@ -1145,9 +1150,9 @@ void launch_dim(const AttnArgs& A, const Plan& p, hipStream_t s) {
     if (p.many) ok = A.c.page_shift >= 6 ? launch_many<T, DIM, true>(A, p.blocks, s) : launch_many<T, DIM, false>(A, p.blocks, s);
   if (!p.many) ok = p.nt == 1 ? launch_few<T, DIM, 1>(A, p.blocks, s) : launch_few<T, DIM, 2>(A, p.blocks, s);
   if (ok && p.splits > 1) {
-    const int64_t out_rows = (int64_t)A.s.tokens * A.heads_q;
-    if (p.splits <= 16) join_kernel<T, DIM, 1><<<dim3((uint32_t)((out_rows + 3) / 4)), dim3(256), 0, s>>>(A, p.rows);
-    else join_kernel<T, DIM, 4><<<dim3((uint32_t)out_rows), dim3(256), 0, s>>>(A, p.rows);
+    const dim3 grid((uint32_t)join_blocks(p, (int64_t)A.s.tokens * A.heads_q));
+    if (p.splits <= kFewSplits) join_kernel<T, DIM, 1><<<grid, dim3(256), 0, s>>>(A, p.rows);
+    else join_kernel<T, DIM, 4><<<grid, dim3(256), 0, s>>>(A, p.rows);
   }
 }
 
@@ -1170,9 +1175,10 @@ int64_t paged_attention_bytes(int64_t tokens, int64_t heads_q, int64_t heads, in
   return (partials(make_plan(heads_q, heads, page, batch, max_q, width, window, dt, dim, true), tokens, heads_q, dim) + 255) / 256 * 256;
 }
 
-int64_t paged_attention_blocks(int64_t heads_q, int64_t heads, int64_t dim, int64_t page, int64_t batch, int64_t max_q, int64_t width,
-                               int64_t window, nvfp4_dtype_t dt) {
-  return make_plan(heads_q, heads, page, batch, max_q, width, window, dt, dim, true).blocks;
+int64_t paged_attention_blocks(int64_t tokens, int64_t heads_q, int64_t heads, int64_t dim, int64_t page, int64_t batch,
+                               int64_t max_q, int64_t width, int64_t window, nvfp4_dtype_t dt) {
+  const Plan p = make_plan(heads_q, heads, page, batch, max_q, width, window, dt, dim, true);
+  return std::max(p.blocks, join_blocks(p, tokens * heads_q));
 }
 
 void launch_paged_attention(const nvfp4_kv_cache_t& c, const void* q, int64_t q_token, int64_t q_head, int64_t heads_q,

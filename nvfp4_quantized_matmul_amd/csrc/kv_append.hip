@@ -42,7 +42,8 @@ struct AppendArgs {
   void* q_out;
   const float* inv_freq;
   int64_t kv_blocks;
-  int32_t heads_q, dim, rot, slots, q_tokens;
+  int32_t heads_q, dim, rot, q_tokens;
+  int32_t slots;   // page slots of a sequence; 0: as the offsets tell
 };
 
 // sin and cos of x >= 0 (below 2^52): x minus the nearest multiple of pi/2 in
@@ -445,7 +446,22 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs A) {
   block >>= 1;
   const int h = (int)(block % A.c.heads);
   block /= A.c.heads;
-  const int slot = (int)(block % A.slots), b = (int)(block / A.slots);
+  int b, slot;
+  if (A.slots > 0) {
+    slot = (int)(block % A.slots);
+    b = (int)(block / A.slots);
+  } else {
+    // the last sequence whose slots start at or before this one
+    const auto start = [&](int i) { return (sequence_row(A.s, i) >> A.c.page_shift) + 2 * i; };
+    int lo = 0, hi = A.s.batch - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (start(mid) <= (int)block) lo = mid; else hi = mid - 1;
+    }
+    b = lo;
+    slot = (int)block - start(b);
+    if (slot < 0) return;
+  }
   const Sequence s = sequence(A.s, b);
   const int first = s.first, stop = s.first + s.count, from = first < 0 ? 0 : first;
   const int64_t pi = (int64_t)(from >> A.c.page_shift) + slot;
@@ -472,6 +488,27 @@ void launch(const AppendArgs& A, bool inter, int64_t blocks, hipStream_t s) {
   else append_kernel<T, W, false><<<dim3((uint32_t)blocks), dim3(kThreads), 0, s>>>(A);
 }
 
+// Page slots that get a block a head and side.  A sequence of n new tokens
+// touches at most ceil(n / page) + 1 pages, one more than they fill when they
+// start inside one; so many for each sequence is little work for a block but
+// many blocks where max_q is far above most sequences' tokens (or not known).
+// Then sequence b has the slots from cu_q[b] / page + 2 b on, at least n / page
+// + 2 of them, and blocks search the sequences for theirs: some dependent loads,
+// taken when they spare more than half of the blocks.  (32 ragged prompts of
+// 8192 tokens together, 8 heads of 128, pages of 16: 58 us searched; 60 us not,
+// with the longest one's tokens as max_q, 239 us with all tokens.  16 of 256: 6.5
+// us, and 7 and 9.)
+struct Slots {
+  int64_t all, each;   // each 0: searched
+};
+Slots page_slots(int64_t page, int64_t tokens, int64_t batch, int64_t max_q) {
+  const int64_t each = (max_q + page - 1) / page + 1, packed = tokens / page + 2 * batch;
+  if (batch * each > 2 * packed) return {packed, 0};
+  return {batch * each, each};
+}
+
+int query_tokens(int64_t tokens) { return tokens > 1024 ? kTokensWide : 1; }
+
 bool wide(const void* p, int64_t a, int64_t b, int64_t size) {
   return ((uintptr_t)p & 15) == 0 && (a * size) % 16 == 0 && (b * size) % 16 == 0;
 }
@@ -481,11 +518,9 @@ bool wide(const void* p, int64_t a, int64_t b, int64_t size) {
 namespace nvfp4host {
 
 int64_t kv_append_blocks(int64_t page, int64_t heads, int64_t heads_q, int64_t tokens, int64_t batch, int64_t max_q) {
-  // pages that max_q tokens can touch: one more than they fill, when they start inside one
-  const int64_t slots = (max_q + page - 1) / page + 1;
   int64_t n;
-  if (__builtin_mul_overflow(batch, slots, &n) || __builtin_mul_overflow(n, heads * 2, &n)) return INT64_MAX;
-  return heads_q > 0 ? n + tokens : n;
+  if (__builtin_mul_overflow(page_slots(page, tokens, batch, max_q).all, heads * 2, &n)) return INT64_MAX;
+  return n + (heads_q > 0 ? (tokens + query_tokens(tokens) - 1) / query_tokens(tokens) : 0);
 }
 
 void launch_kv_append(const nvfp4_kv_cache_t& c, const void* k, int64_t k_token, int64_t k_head, const void* v,
@@ -501,10 +536,11 @@ void launch_kv_append(const nvfp4_kv_cache_t& c, const void* k, int64_t k_token,
   A.q_out = q_out;
   A.inv_freq = inv_freq;
   A.heads_q = (int32_t)heads_q; A.dim = (int32_t)c.dim; A.rot = (int32_t)rot;
-  A.slots = (int32_t)((max_q + c.page - 1) / c.page + 1);
-  A.kv_blocks = batch * A.slots * c.heads * 2;
-  A.q_tokens = tokens > 1024 ? kTokensWide : 1;
-  const int64_t blocks = A.kv_blocks + (heads_q > 0 ? (tokens + A.q_tokens - 1) / A.q_tokens : 0);
+  const Slots slots = page_slots(c.page, tokens, batch, max_q);
+  A.slots = (int32_t)slots.each;
+  A.kv_blocks = slots.all * c.heads * 2;
+  A.q_tokens = query_tokens(tokens);
+  const int64_t blocks = kv_append_blocks(c.page, c.heads, heads_q, tokens, batch, max_q);
   // 16-byte accesses where every row and half of a rotated head starts on one
   const int64_t size = dt == NVFP4_F32 ? 4 : 2;
   const bool vec = rot % 16 == 0 && wide(k, k_token, k_head, size) && wide(v, v_token, v_head, size) &&

@@ -30,12 +30,17 @@ struct Sequence {
   int32_t first;        // position of the first of them; lengths may pass the table
 };
 
+// The first row of sequence b.
+__device__ __forceinline__ int sequence_row(const SequenceView& sv, int b) {
+  const int lo = sv.cu ? sv.cu[b] : b;
+  return lo < 0 ? 0 : lo > sv.tokens ? sv.tokens : lo;
+}
+
 // Sequence b, its rows cut to the rows that exist and to those that the call takes.
 __device__ __forceinline__ Sequence sequence(const SequenceView& sv, int b) {
   Sequence s;
-  int lo = sv.cu ? sv.cu[b] : b, hi = sv.cu ? sv.cu[b + 1] : b + 1;
-  const int len = sv.lens[b];
-  lo = lo < 0 ? 0 : lo > sv.tokens ? sv.tokens : lo;
+  const int lo = sequence_row(sv, b), len = sv.lens[b];
+  int hi = sv.cu ? sv.cu[b + 1] : b + 1;
   hi = hi < lo ? lo : hi > sv.tokens ? sv.tokens : hi;
   s.row0 = lo;
   s.first = (len < 0 ? 0 : len) - (hi - lo);

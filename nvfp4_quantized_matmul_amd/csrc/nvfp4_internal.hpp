@@ -127,7 +127,7 @@ void launch_gather(const void* x, nvfp4_dtype_t dt, int64_t X, int64_t M, int64_
                    void* out, hipStream_t s);
 
 // Appends new tokens to the paged 8-bit cache and rotates queries (heads_q 0:
-// none); kv_append_blocks is an upper bound of its grid.
+// none); kv_append_blocks is its grid.
 int64_t kv_append_blocks(int64_t page, int64_t heads, int64_t heads_q, int64_t tokens, int64_t batch, int64_t max_q);
 void launch_kv_append(const nvfp4_kv_cache_t& c, const void* k, int64_t k_token, int64_t k_head, const void* v,
                       int64_t v_token, int64_t v_head, const void* q, int64_t q_token, int64_t q_head,
@@ -135,11 +135,12 @@ void launch_kv_append(const nvfp4_kv_cache_t& c, const void* k, int64_t k_token,
                       int64_t batch, int64_t max_q, const int32_t* table, int64_t width, const int32_t* lens,
                       const float* inv_freq, int64_t rot, bool inter, hipStream_t s);
 // Attention over the paged cache.  paged_attention_bytes is the workspace that
-// a split of the token axis wants (0: none), paged_attention_blocks its grid.
+// a split of the token axis wants (0: none), paged_attention_blocks the larger
+// one of its grids.
 int64_t paged_attention_bytes(int64_t tokens, int64_t heads_q, int64_t heads, int64_t dim, int64_t page, int64_t batch,
                               int64_t max_q, int64_t width, int64_t window, nvfp4_dtype_t dt);
-int64_t paged_attention_blocks(int64_t heads_q, int64_t heads, int64_t dim, int64_t page, int64_t batch, int64_t max_q, int64_t width,
-                               int64_t window, nvfp4_dtype_t dt);
+int64_t paged_attention_blocks(int64_t tokens, int64_t heads_q, int64_t heads, int64_t dim, int64_t page, int64_t batch,
+                               int64_t max_q, int64_t width, int64_t window, nvfp4_dtype_t dt);
 void launch_paged_attention(const nvfp4_kv_cache_t& c, const void* q, int64_t q_token, int64_t q_head, int64_t heads_q,
                             nvfp4_dtype_t dt, int64_t tokens, const int32_t* cu, int64_t batch, int64_t max_q,
                             const int32_t* table, int64_t width, const int32_t* lens, int64_t window, float scale,
@@ -154,5 +155,7 @@ void launch_sample(const void* logits, nvfp4_dtype_t dt, int64_t batch, int64_t 
 // Grid limits used by the launchers (HIP: gridDim.x < 2^31, y/z < 2^16).
 constexpr int64_t kMaxGridX = 2147483647LL;
 constexpr int64_t kMaxGridY = 65535;
+// ... and less than 2^32 threads in a dimension: blocks of 256.
+constexpr int64_t kMaxGrid256 = 0xffffffffLL / 256;
 
 }  // namespace nvfp4host

@@ -113,7 +113,7 @@ int nvfp4_kv_append(const nvfp4_kv_cache_t* cache, const void* k, int64_t k_toke
     if (overlaps(q_out, no, q, nq) || overlaps(q_out, no, k, nk) || overlaps(q_out, no, v, nv)) return NVFP4_ERR_SHAPE;
     if (overlaps(q_out, no, cache->k, cache_bytes) || overlaps(q_out, no, cache->v, cache_bytes)) return NVFP4_ERR_SHAPE;
   }
-  if (nvfp4host::kv_append_blocks(cache->page, cache->heads, heads_q, tokens, batch, max_q) > nvfp4host::kMaxGridX)
+  if (nvfp4host::kv_append_blocks(cache->page, cache->heads, heads_q, tokens, batch, max_q) > nvfp4host::kMaxGrid256)
     return NVFP4_ERR_GRID;
   nvfp4host::launch_kv_append(*cache, k, k_token, k_head, v, v_token, v_head, q, q_token, q_head, heads_q, q_out, dtype,
                               tokens, cu_q, batch, max_q, table, table_width, lens, inv_freq, rot, interleaved != 0, stream);
@@ -164,8 +164,8 @@ int nvfp4_paged_attention(const nvfp4_kv_cache_t* cache, const void* q, int64_t 
                     overlaps(workspace, workspace_bytes, cache->k, cache_bytes) ||
                     overlaps(workspace, workspace_bytes, cache->v, cache_bytes)))
     return NVFP4_ERR_SHAPE;
-  if (nvfp4host::paged_attention_blocks(heads_q, cache->heads, cache->dim, cache->page, batch, max_q, table_width, window, dtype) >
-      nvfp4host::kMaxGridX)
+  if (nvfp4host::paged_attention_blocks(tokens, heads_q, cache->heads, cache->dim, cache->page, batch, max_q, table_width, window,
+                                        dtype) > nvfp4host::kMaxGrid256)
     return NVFP4_ERR_GRID;
   nvfp4host::launch_paged_attention(*cache, q, q_token, q_head, heads_q, dtype, tokens, cu_q, batch, max_q, table,
                                     table_width, lens, window, scale, workspace, workspace_bytes, out, stream);

@@ -8,7 +8,7 @@ import torch
 
 import nvfp4_quantized_matmul_amd as nv
 from gpu_util import DEV, guarded
-from test_serving_gpu import BF16, E4M3, F16, F32, check_attention, make_cache, paging, to_gpu
+from test_serving_gpu import BF16, E4M3, F16, F32, check_attention, make_cache, paging, run_append, to_gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -93,6 +93,53 @@ def test_windows_around_the_table(dtype, hq, count, window):
 @pytest.mark.parametrize("window", [3000, 6400, 6500])
 def test_windows_around_a_split_table(dtype, hq, count, window):
     run(4, dtype, hq, 1, 64, 64, 100, [6300, 7000, 9500, 13000], [count] * 4, window)
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,dim,page,firsts,counts,rot,interleaved", [
+    (BF16, 4, 2, 64, 16, [5, 0, 9, 30, 15, 16, 7, 0, 1], [300, 1, 0, 17, 40, 0, 64, 3, 2], 64, False),
+    (F32, 2, 1, 64, 16, [0] * 6 + [15], [1, 1, 1, 1, 1, 1, 200], 32, True),
+    (F16, 3, 3, 128, 32, [31, 0, 0, 0, 100, 0, 0, 3], [0, 0, 500, 0, 1, 0, 0, 0], 128, False)])
+@pytest.mark.parametrize("bound", [True, False])
+def test_append_of_ragged_sequences(dtype, hq, hkv, dim, page, firsts, counts, rot, interleaved, bound, monkeypatch):
+    """One long sequence among short and empty ones, with and without a bound of their new tokens."""
+    real = nv.kv_append
+    if not bound:
+        monkeypatch.setattr(nv, "kv_append", lambda *a, max_q=None, **k: real(*a, **k))
+    run_append(21, dtype, hq, hkv, dim, page, firsts, counts, rot, interleaved)
+
+
+def test_append_without_a_bound_of_many_tokens():
+    """64 ragged prompts of 131072 tokens together, in pages of 16 and 16 heads:
+    a block for each page that each of them might have would be 16.8 million."""
+    g = torch.Generator().manual_seed(8)
+    batch, tokens, heads, page, dim = 64, 131072, 16, 16, 64
+    ends = torch.cat((torch.randint(0, tokens + 1, (batch - 1,), generator=g).sort().values, torch.tensor([tokens])))
+    cu = torch.cat((torch.zeros(1, dtype=torch.int64), ends))
+    counts = cu[1:] - cu[:-1]
+    firsts = torch.randint(0, 40, (batch,), generator=g)
+    lens = firsts + counts
+    need = -(-lens // page)
+    table = torch.full((batch, int(need.max())), -1, dtype=torch.int32)
+    at = 0
+    for b, n in enumerate(need.tolist()):
+        table[b, :n] = torch.arange(at, at + n)
+        at += n
+    k = torch.randn(tokens, heads, dim, device=DEV).to(BF16)
+    v = torch.randn(tokens, heads, dim, device=DEV).to(BF16)
+    print("append", batch, tokens, heads, page, dim, flush=True)
+    a, b = nv.KVCache.empty(at, heads, page, dim), nv.KVCache.empty(at, heads, page, dim)
+    nv.kv_append(k, v, a, table.to(DEV), i32(lens.tolist()), cu_q=i32(cu.tolist()))
+    nv.kv_append(k, v, b, table.to(DEV), i32(lens.tolist()), cu_q=i32(cu.tolist()), max_q=int(counts.max()))
+    for x, y in ((a.k, b.k), (a.v, b.v), (a.k_scales, b.k_scales), (a.v_scales, b.v_scales)):
+        assert torch.equal(x, y)
+    # every new token is there: the values' codes against the definition
+    seq = torch.searchsorted(cu[1:], torch.arange(tokens), right=True)
+    pos = torch.arange(tokens) - cu[seq] + firsts[seq]
+    pid = table[seq, pos // page].long().to(DEV)
+    codes = a.v[pid, :, :, (pos % page).to(DEV)]
+    scale = torch.exp2(a.v_scales[pid].double() - 127)[..., None]
+    got = E4M3.to(DEV)[codes.int()] * scale
+    assert ((got - v.double()).abs() <= torch.maximum(2.0 ** -4 * v.double().abs(), 2.0 ** -10 * scale)).all()
 
 
 # few rows and many, one split, up to 16 (one wave joins) and more (four)
