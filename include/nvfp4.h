@@ -453,7 +453,7 @@ typedef struct nvfp4_kv_cache {
  *   k, v    [tokens, heads, dim] of dtype, strides k_token, k_head, v_token,
  *           v_head
  *   q       [tokens, heads_q, dim] of dtype, strides q_token, q_head, or NULL
- *           (then q_out is NULL too)
+ *           (then q_out is NULL too); heads_q is at most 2^20
  *   q_out   [tokens, heads_q, dim] of dtype, contiguous, 16-byte aligned
  *   inv_freq float [rot / 2] or NULL with rot 0: channels [0, rot) (rot even,
  *           at most dim) of token position p turn by the angles p * inv_freq[i].

@@ -21,6 +21,9 @@ int launched() { return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_H
 
 // Positions are 32-bit in the kernels, with room for a tile past the end.
 constexpr int64_t kMaxPositions = 1LL << 30;
+// A block of the append turns up to four tokens' query heads, of up to 128 items
+// each, in a 32-bit index.
+constexpr int64_t kMaxTurnedHeads = 1LL << 20;
 
 // Elements from the first to behind the last one of [tokens, heads, dim] with
 // these strides.
@@ -94,6 +97,7 @@ int nvfp4_kv_append(const nvfp4_kv_cache_t* cache, const void* k, int64_t k_toke
   if ((q != nullptr) != (q_out != nullptr)) return NVFP4_ERR_SHAPE;
   if (k_token < 0 || k_head < 0 || v_token < 0 || v_head < 0 || q_token < 0 || q_head < 0) return NVFP4_ERR_SHAPE;
   if (!q) heads_q = 0;
+  if (heads_q > kMaxTurnedHeads) return NVFP4_ERR_SHAPE;
   if (!cu_q && tokens != batch) return NVFP4_ERR_SHAPE;
   if (tokens == 0 || batch == 0) return NVFP4_OK;
   if (max_q == 0) return NVFP4_ERR_SHAPE;   // new tokens, and none in any sequence

@@ -23,6 +23,12 @@ def test_attention_grids_in_threads(lib, sizes):  # noqa: F811
     assert attention(lib, c=apart(heads=2 if sizes["hq"] == 2 else 32), out=4 * FAR, **sizes) == GRID
 
 
+@pytest.mark.parametrize("heads_q", [(1 << 20) + 1, (1 << 24) - 1, 1 << 27])
+def test_append_query_heads(lib, heads_q):  # noqa: F811
+    """4 tokens of 2^24 heads and more have more items than a 32-bit index counts."""
+    assert append(lib, c=apart(), tokens=1, batch=1, max_q=1, hq=heads_q, out=4 * FAR, q=8 * FAR) == SHAPE
+
+
 @pytest.mark.parametrize("sizes,heads", [
     (dict(tokens=1 << 18, batch=2, max_q=1 << 18), 4096),
     (dict(tokens=1 << 18, batch=1 << 18, max_q=1), 32),
