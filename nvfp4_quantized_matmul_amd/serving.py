@@ -42,10 +42,24 @@ class KVCache:
     hold E4M3 codes; k_scales and v_scales uint8 [pages, heads] the power of
     two (exponent + 127) that a page's codes of one head are multiplied by.
     page is 16, 32, 64, 128 or 256, dim 64, 128, 192 or 256.  The tensors are
-    contiguous, on one GPU, and stay the caller's: the object only names them.
+    contiguous, on one GPU, and stay the caller's: the object only names them,
+    by the addresses that they have when it is made, so its attributes cannot be
+    assigned.
     """
 
-    __slots__ = ("k", "v", "k_scales", "v_scales", "pages", "heads", "page", "dim", "device", "index", "_struct", "_ref")
+    __slots__ = ("_k", "_v", "_k_scales", "_v_scales", "_pages", "_heads", "_page", "_dim", "_device", "_index",
+                 "_struct", "_ref")
+
+    k = property(lambda self: self._k, doc="codes of the keys")
+    v = property(lambda self: self._v, doc="codes of the values")
+    k_scales = property(lambda self: self._k_scales, doc="scales of the keys")
+    v_scales = property(lambda self: self._v_scales, doc="scales of the values")
+    pages = property(lambda self: self._pages, doc="pages of the pool")
+    heads = property(lambda self: self._heads, doc="key/value heads")
+    page = property(lambda self: self._page, doc="tokens of a page")
+    dim = property(lambda self: self._dim, doc="channels of a head")
+    device = property(lambda self: self._device, doc="the tensors' device")
+    index = property(lambda self: self._index, doc="the device's index")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor):
         shape, index = k.shape, k.get_device()
@@ -68,9 +82,9 @@ class KVCache:
             raise ValueError("the cache's tensors must be on the same device")
         if index < 0:
             raise ValueError("the cache's tensors must be on the GPU")
-        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
-        self.pages, self.heads, self.page, self.dim, self.index = pages, heads, page, dim, index
-        self.device = k.device
+        self._k, self._v, self._k_scales, self._v_scales = k, v, k_scales, v_scales
+        self._pages, self._heads, self._page, self._dim, self._index = pages, heads, page, dim, index
+        self._device = k.device
         self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
                                     pages, heads, page, dim)
         self._ref = ctypes.addressof(self._struct)
@@ -89,9 +103,9 @@ def _refuse_tokens(name: str, x: torch.Tensor, cache: KVCache, tokens: int, head
     """Raises for a tensor of new tokens that is not [tokens, heads, dim]."""
     if x.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
-    if x.shape != (tokens, heads, cache.dim):
-        raise ValueError(f"{name} {tuple(x.shape)} must be {(tokens, heads, cache.dim)} ([tokens, heads, dim])")
-    if x.get_device() != cache.index:
+    if x.shape != (tokens, heads, cache._dim):
+        raise ValueError(f"{name} {tuple(x.shape)} must be {(tokens, heads, cache._dim)} ([tokens, heads, dim])")
+    if x.get_device() != cache._index:
         raise ValueError(f"{name} must be on the cache's device")
     raise ValueError(f"{name}'s last axis must be contiguous")
 
@@ -102,7 +116,7 @@ def _refuse_sequences(cache: KVCache, **tensors: Optional[torch.Tensor]) -> None
             continue
         if t.dtype is not _I32:
             raise TypeError(f"{name} must be int32, got {t.dtype}")
-        if t.get_device() != cache.index:
+        if t.get_device() != cache._index:
             raise ValueError(f"{name} must be on the cache's device")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
@@ -112,7 +126,7 @@ def _refuse_sequences(cache: KVCache, **tensors: Optional[torch.Tensor]) -> None
 def _sequences(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, cu_q: Optional[torch.Tensor],
                max_q: Optional[int], tokens: int):
     """(batch, width, max_q, address of cu_q) of the sequences' tensors, checked."""
-    index, shape = cache.index, table.shape
+    index, shape = cache._index, table.shape
     if not (len(shape) == 2 and lens.shape == (shape[0],) and table.dtype is _I32 and lens.dtype is _I32
             and table.get_device() == index == lens.get_device() and table.is_contiguous() and lens.is_contiguous()):
         _refuse_sequences(cache, table=table, lens=lens)
@@ -132,8 +146,8 @@ def _sequences(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, cu_q: Op
 
 def _output(out: Optional[torch.Tensor], q: torch.Tensor, shape, cache: KVCache) -> torch.Tensor:
     if out is None:
-        return torch.empty(shape, dtype=q.dtype, device=cache.device)
-    if out.dtype is not q.dtype or out.shape != shape or not out.is_contiguous() or out.get_device() != cache.index:
+        return torch.empty(shape, dtype=q.dtype, device=cache._device)
+    if out.dtype is not q.dtype or out.shape != shape or not out.is_contiguous() or out.get_device() != cache._index:
         raise ValueError("out must be contiguous, of q's dtype, shape and device")
     return out
 
@@ -159,15 +173,15 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, table: torch.Ten
     that it held are then rounded anew; the values of a page at one scale are
     off by at most half a step of their codes.
     """
-    dtype, shape, index, dim = k.dtype, k.shape, cache.index, cache.dim
+    dtype, shape, index, dim = k.dtype, k.shape, cache._index, cache._dim
     code = _dtype_code(dtype)
     tokens = shape[0] if len(shape) else 0
-    want = (tokens, cache.heads, dim)
+    want = (tokens, cache._heads, dim)
     ks, vs = k.stride(), v.stride()
     if not (shape == want and k.get_device() == index and (ks[2] == 1 or tokens == 0)):
-        _refuse_tokens("k", k, cache, tokens, cache.heads, dtype)
+        _refuse_tokens("k", k, cache, tokens, cache._heads, dtype)
     if not (v.shape == want and v.dtype is dtype and v.get_device() == index and (vs[2] == 1 or tokens == 0)):
-        _refuse_tokens("v", v, cache, tokens, cache.heads, dtype)
+        _refuse_tokens("v", v, cache, tokens, cache._heads, dtype)
     batch, width, most, cu = _sequences(cache, table, lens, cu_q, max_q, tokens)
     rot, freq = 0, None
     if inv_freq is not None:
@@ -199,7 +213,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, table: torch.Ten
     _check("nvfp4_kv_append", load_library().nvfp4_kv_append(
         cache._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], qp, q_token, q_head, heads_q, qo, code,
         tokens, cu, batch, most, table.data_ptr(), width, lens.data_ptr(), freq, rot, 1 if interleaved else 0,
-        _stream(cache.device)))
+        _stream(cache._device)))
     return out
 
 
@@ -220,10 +234,10 @@ def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
     zeros for a query that sees nothing.
     """
     code = _dtype_code(q.dtype)
-    shape, heads, dim = q.shape, cache.heads, cache.dim
+    shape, heads, dim = q.shape, cache._heads, cache._dim
     tokens, heads_q = (shape[0], shape[1]) if len(shape) == 3 else (0, 0)
     qs = q.stride()
-    if not (shape == (tokens, heads_q, dim) and q.get_device() == cache.index
+    if not (shape == (tokens, heads_q, dim) and q.get_device() == cache._index
             and (qs[2] == 1 or tokens == 0 or heads_q == 0)):
         _refuse_tokens("q", q, cache, tokens, heads_q, q.dtype)
     if heads_q % heads != 0:
@@ -233,7 +247,7 @@ def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
     if tokens == 0 or heads_q == 0:
         return out
     lib = load_library()
-    key = (tokens, heads_q, heads, dim, cache.page, batch, most, width, window, code)
+    key = (tokens, heads_q, heads, dim, cache._page, batch, most, width, window, code)
     ws_bytes = _ATTENTION_WS_CACHE.get(key)
     if ws_bytes is None:
         ws_bytes = int(lib.nvfp4_paged_attention_workspace_size(*key))
@@ -241,11 +255,11 @@ def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
             raise NVFP4Error("nvfp4_paged_attention_workspace_size", ws_bytes)
         if len(_ATTENTION_WS_CACHE) < 4096:
             _ATTENTION_WS_CACHE[key] = ws_bytes
-    ws = torch.empty(ws_bytes, dtype=_U8, device=cache.device) if ws_bytes else None
+    ws = torch.empty(ws_bytes, dtype=_U8, device=cache._device) if ws_bytes else None
     _check("nvfp4_paged_attention", lib.nvfp4_paged_attention(
         cache._ref, q.data_ptr(), qs[0], qs[1], heads_q, code, tokens, cu, batch, most, table.data_ptr(), width,
         lens.data_ptr(), window, dim ** -0.5 if scale is None else scale, ws.data_ptr() if ws_bytes else None, ws_bytes,
-        out.data_ptr(), _stream(cache.device)))
+        out.data_ptr(), _stream(cache._device)))
     return out
 
 
