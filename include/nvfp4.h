@@ -465,9 +465,9 @@ typedef struct nvfp4_kv_cache {
  * the page's present scale if that is larger and the page holds earlier
  * tokens of the sequence, whose codes are then rounded anew at the grown
  * scale.  Values that are not finite become NaN codes.  Codes behind a
- * sequence's last token keep what they held.  The angles are formed and
- * reduced in 64 bits, so far positions lose nothing; each value is rounded
- * to 32 bits after its rotation and then once to its code, or to q_out.
+ * sequence's last token keep what they held.  The angles (up to 2^52) are
+ * formed and reduced in 64 bits, so far positions lose nothing; each value is
+ * rounded to 32 bits after its rotation and then once to its code, or to q_out.
  * Pages that a call writes must belong to one sequence each.
  */
 int nvfp4_kv_append(const nvfp4_kv_cache_t* cache, const void* k, int64_t k_token, int64_t k_head,
@@ -526,9 +526,11 @@ int nvfp4_paged_attention(const nvfp4_kv_cache_t* cache, const void* q, int64_t 
  * before them; min_p those with w >= min_p; the first one always stays.  The
  * result is the first kept token, by index, whose running sum of w exceeds u
  * times the kept ones' sum.  NaN logits count as -inf; a row with nothing
- * above -inf gives token -1 and probability 0.  Weights and sums are in 64
- * bits (the sums that place the top_p border in 62-bit fixed point), added in
- * a fixed order: results repeat bit for bit.
+ * above -inf gives token -1 and probability 0.  Weights (good to 1e-11) and
+ * their sums are in 64 bits.  The sums that place the top_p border are of
+ * weights rounded to integers, good to 2e-10 of the whole, or to vocab^2 2^-62
+ * of it in rows with many equal or nearly equal logits at the border.  Nothing
+ * depends on an order that may change: results repeat bit for bit.
  *
  * workspace (device, 16-byte aligned, of at least
  * nvfp4_sample_workspace_size bytes) lets several blocks share a row;

@@ -75,6 +75,13 @@ struct Mma<_Float16> {
   }
 };
 
+// Weights of the 2-byte types are rounded once to their type, as the queries
+// are; sums are of the weights as they were.  Against 64 bits a bf16 output is
+// then off by 2.1e-3 of its norm, 1.7e-3 of it the output's own rounding (f16
+// 2.9e-4, 2.1e-4).  A second part of each weight takes that away, but costs a
+// prompt of 4096 tokens 26% (280 us, 42 heads of 128), single tokens 1% at 128
+// channels and 12% at 192; a row is to come out alike from either kernel.
+//
 // The range of weights.  In bf16 and float32 they reach 1 or a little more.  f16
 // has its 11 bits down to 2^-14 only and nothing below 2^-25: there r lies below
 // m, weights reach 2^15, and one of 2^-25 of the largest still has all its bits;
@@ -229,10 +236,11 @@ __device__ __forceinline__ Span span_of(const AttnArgs& A, const Sequence& s, in
 // between waves until the end, so K and V go straight from memory to
 // registers; the queries lie in LDS as operands.
 //
-// Bound by memory: 4 sequences of up to 128k tokens (837 MB) take 165 us, 5.1
-// TB/s, where a copy of 2 GiB reaches 4.95; 32 of up to 8k 28 us, 3.1 TB/s and
-// 4 us of it the join.  Loads that bypass the caches took 193 us for the
-// former: in pages of 128 tokens two waves share each line of the values.
+// Bound by memory: 4 sequences of up to 128k tokens (837 MB) take 165 us with
+// the join, 5.1 TB/s, where a plain read of as much reaches 6.5 and a copy 4.9;
+// 32 of up to 8k 28 us, 3.1 TB/s and 5 us of it the join.  Loads that bypass
+// the caches took 193 us for the former: in pages of 128 tokens two waves share
+// each line of the values.
 constexpr int kFewWaves = 4;
 
 template <int DIM, int NT, int PARTS>
@@ -242,8 +250,12 @@ constexpr int few_lds_bytes() {
   return q > red ? q : red;
 }
 
-// Registers a lane needs for the running sums, a tile's scores and its codes:
-// past what two blocks a unit leave each, one block has them all.
+// About what registers a lane needs for the running sums, a tile's scores and
+// its codes: up to what two blocks a unit leave each there are two.  The
+// compiler does not always meet it: 2-byte types with 16 rows of 192 channels
+// spill 25 at two blocks (32 sequences of up to 8k tokens, 16 heads, take 38 us,
+// 41 with one block and no spill; 4 of up to 87k 199 us, and 183), 32 rows of
+// 256 spill 82, and 107 in float32, at one.
 template <int DIM, int NT, int PARTS>
 constexpr int few_blocks_per_cu() { return NT * DIM / 4 + 16 * NT + DIM / 2 + 24 * PARTS * NT + 64 <= 256 ? 2 : 1; }
 
@@ -620,13 +632,14 @@ __global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>:
 // The reference is raised only once a score passes it by kMostMany: most tiles
 // leave the sums alone.
 //
-// Bound by the vector units beside the matrix cores: a wave's tile is 32
-// exponentials, 16 maxima, 32 scalings, 32 sums and 16 conversions a lane
-// (about 1100 cycles) to 1024 (dim 128) or 512 (dim 64) of multiplies, and two
-// or three waves a SIMD overlap them in part.  A causal prompt of 4096 tokens,
-// 42 heads of 128, takes 244 us (740 TFLOP/s); 1024 tokens over 32768, 16
-// heads of 64, 229 us (591 TFLOP/s).  Two groups of four waves that took turns
-// at multiplies and weights over the same tile measured 256 and 273 us.
+// Bound by the order of a wave's steps, not by a unit: K Q^T, the maximum, the
+// weights and V P^T follow one another, and the two or three waves a SIMD that
+// the registers leave overlap little of it.  A causal prompt of 4096 tokens, 42
+// heads of 128, takes 225 us (803 TFLOP/s), with the matrix cores busy 32% of
+// the cycles, the vector units 45%, and waves waiting 31% of theirs; 1024 tokens
+// over 32768, 16 heads of 64, 214 us with the join (631 TFLOP/s; 26%, 59% and
+// 32%).  Two groups of four waves that took turns at multiplies and weights
+// over the same tile took 5% and 19% longer.
 constexpr int kManyWaves = 4, kManyRows = 32 * kManyWaves;
 
 template <typename T>

@@ -23,9 +23,13 @@
 // for the sums, 11 for the choice.
 //
 // With a quarter of a million tokens a probability is a millionth and the
-// place of u among them is decided in the 7th digit and beyond, so weights and
-// running sums are in 64 bits.  A histogram's sums are integers, which add up
-// the same in any order; everything else is added in a fixed order.
+// place of u among them is decided in the 7th digit and beyond, so weights (good
+// to 1e-11) and running sums are in 64 bits.  A histogram's sums are integers,
+// which add up the same in any order; everything else is added in a fixed order.
+// The place of top-p's border comes from them: with bins a token's weight is
+// rounded to 2^-32 of its bin's largest, so that the sums are good to 2e-10;
+// by digits to 2^-(62 - bits of the vocabulary), good to vocabulary^2 2^-62 of a
+// row's sum (1.5e-8 for a quarter of a million, 2e-10 for 32000).
 #include "nvfp4_device.hpp"
 #include "nvfp4_internal.hpp"
 
@@ -67,7 +71,7 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 
 // 2^y, y in [-kFar, kFar]: the power of two of the nearest integer and the
 // Taylor sum of the rest to its 9th power, whose first left-out term is below
-// 8e-12 of the sum.
+// 1e-11 of the sum.
 constexpr double kFar = 1080.0;   // weights below 2^-kFar are 0
 __device__ __forceinline__ double exp2_64(double y) {
   const double n = __builtin_rint(y), f = (y - n) * 0.69314718055994530942;
