@@ -509,6 +509,96 @@ int nvfp4_paged_attention(const nvfp4_kv_cache_t* cache, const void* q, int64_t 
                           int64_t workspace_bytes, void* out, hipStream_t stream);
 
 /*
+ * Pages of the cache, kept on the device: which of them are free, which ones a
+ * sequence has, and sequences that share theirs.  The caches of all layers
+ * (nvfp4_kv_cache_t caches[count], of one geometry) go by one table and one
+ * count:
+ *
+ *   table  int32 [batch, width]: the pages of each sequence, in order; an entry
+ *          outside [0, pages) names none, and the calls write -1 for it
+ *   refs   int32 [pages]: the entries of the table that name a page; a page
+ *          whose count is not above 0 is free.  The caller may count references
+ *          of its own.
+ *
+ * A new table is all -1 with counts 0.  A decode step that moves on in lens
+ * calls nvfp4_kv_free for what it no longer needs, then nvfp4_kv_reserve for
+ * the new tokens' pages, then the append and the attention of each layer.  Like
+ * those the calls read table, lens and offsets on the device only, stay inside
+ * the buffers whatever they hold, and give the same results every time.  The
+ * buffers of a call must not overlap.  A table has at most 2^31 - 1 entries.
+ */
+
+/*
+ * nvfp4_kv_free -- gives back the pages that hold nothing that is needed: entry
+ * i of sequence b stays if its page begins before lens[b], and with keep > 0 if
+ * besides it ends behind lens[b] - keep or begins before `sinks`.  Another
+ * entry that names a page is set to -1 and the page's count falls by one.
+ *
+ * A sequence that has ended has lens[b] 0.  A window of w tokens with one new
+ * token a step needs keep = w, with n new ones w + n - 1.
+ */
+int nvfp4_kv_free(int32_t* table, int64_t batch, int64_t width, const int32_t* lens, int64_t page, int64_t keep,
+                  int64_t sinks, int32_t* refs, int64_t pages, hipStream_t stream);
+
+/*
+ * nvfp4_kv_reserve -- pages for the new tokens of each sequence (lens, cu_q,
+ * tokens as for nvfp4_kv_append; rows outside [0, tokens) are left out).
+ *
+ * An entry that new tokens reach needs a page where it names none, or one that
+ * is named more than once: new tokens are never written into a page that
+ * another sequence reads.  Free pages go, the lowest first, to the entries that
+ * need one in the order of (sequence, entry); counts become 1, those of shared
+ * pages fall by one.  Where earlier tokens of the sequence share a page with
+ * new ones its contents are copied, in all caches; the contents of other pages
+ * are not changed.
+ *
+ * missing int32 [batch]: 0, or the pages that a sequence needs where they, with
+ * those of the sequences before it, are more than there are free ones: then
+ * all of its entries stay as they were.  No token may be appended to it before
+ * a later call has served it: it may still share the page it would be written to.
+ *
+ * workspace: device, 16-byte aligned, of at least
+ * nvfp4_kv_reserve_workspace_size bytes.
+ */
+int64_t nvfp4_kv_reserve_workspace_size(int64_t tokens, int64_t batch, int64_t page);
+int nvfp4_kv_reserve(const nvfp4_kv_cache_t* caches, int64_t count, int32_t* table, int64_t batch, int64_t width,
+                     const int32_t* lens, const int32_t* cu_q, int64_t tokens, int32_t* refs, void* workspace,
+                     int64_t workspace_bytes, int32_t* missing, hipStream_t stream);
+
+/*
+ * nvfp4_kv_fork -- a table whose row r is row parent[r] of the present one, and
+ * whose lengths are those rows': sequences that go on from others (samples of
+ * one prompt, the beams of a search), sharing their pages.  A parent outside
+ * [0, batch) gives a row of -1 and length 0; rows that are nobody's parent are
+ * dropped.  Counts rise with the entries of the new table and fall with those
+ * of the present one, which is not used any more.
+ *
+ *   parent     int32 [rows]
+ *   table_out  int32 [rows, width], lens_out int32 [rows]
+ */
+int nvfp4_kv_fork(const int32_t* table, int64_t batch, int64_t width, const int32_t* lens, const int32_t* parent,
+                  int64_t rows, int32_t* refs, int64_t pages, int32_t* table_out, int32_t* lens_out,
+                  hipStream_t stream);
+
+/*
+ * nvfp4_kv_compact -- moves the pages in use (counts above 0) to the front of
+ * the pool: with `used` of them, the k-th page in use at or behind `used` goes
+ * to the k-th free one before it, in all caches, with its count; the table's
+ * entries follow.  Contents of pages that are left stay there.
+ *
+ *   used   int32 [1]
+ *   where  int32 [pages]: the place of each page that was in use, -1 for the
+ *          others
+ *
+ * workspace: device, 16-byte aligned, of at least
+ * nvfp4_kv_compact_workspace_size bytes.
+ */
+int64_t nvfp4_kv_compact_workspace_size(int64_t pages);
+int nvfp4_kv_compact(const nvfp4_kv_cache_t* caches, int64_t count, int32_t* table, int64_t batch, int64_t width,
+                     int32_t* refs, void* workspace, int64_t workspace_bytes, int32_t* used, int32_t* where,
+                     hipStream_t stream);
+
+/*
  * nvfp4_sample -- one token per row from its logits and a given random number.
  *
  *   logits       [batch, vocab] of dtype, row stride row_stride (elements)

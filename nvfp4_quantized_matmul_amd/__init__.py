@@ -26,6 +26,7 @@ __all__ = [
     "qmm_batched", "qmm_glu", "gather_qmm", "select_route", "qmv_max_rows", "status_string",
     "ROUTE_AUTO", "ROUTE_QMV", "ROUTE_GEMM", "GLU_ACTIVATIONS",
     "KVCache", "kv_append", "paged_attention", "sample",
+    "kv_free", "kv_reserve", "kv_fork", "kv_compact",
 ]
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -87,6 +88,12 @@ def load_library() -> ctypes.CDLL:
                                   vp, i64, vp, vp],
         "nvfp4_sample_workspace_size": [i64, i64, c_int],
         "nvfp4_sample": [vp, c_int, i64, i64, i64, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp],
+        "nvfp4_kv_free": [vp, i64, i64, vp, i64, i64, i64, vp, i64, vp],
+        "nvfp4_kv_reserve_workspace_size": [i64, i64, i64],
+        "nvfp4_kv_reserve": [vp, i64, vp, i64, i64, vp, vp, i64, vp, vp, i64, vp, vp],
+        "nvfp4_kv_fork": [vp, i64, i64, vp, vp, i64, vp, i64, vp, vp, vp],
+        "nvfp4_kv_compact_workspace_size": [i64],
+        "nvfp4_kv_compact": [vp, i64, vp, i64, i64, vp, vp, i64, vp, vp, vp],
         "nvfp4_select_route": [i64, i64, i64, c_int, c_int],
         "nvfp4_qmv_max_rows": [],
         "nvfp4_status_string": [c_int],
@@ -102,6 +109,8 @@ def load_library() -> ctypes.CDLL:
     lib.nvfp4_static_scratch_bytes.restype = i64
     lib.nvfp4_paged_attention_workspace_size.restype = i64
     lib.nvfp4_sample_workspace_size.restype = i64
+    lib.nvfp4_kv_reserve_workspace_size.restype = i64
+    lib.nvfp4_kv_compact_workspace_size.restype = i64
     lib.nvfp4_status_string.restype = ctypes.c_char_p
     _lib = lib
     return lib
@@ -154,6 +163,18 @@ def _stream(device: torch.device):
     if _RAW_STREAM is not None:
         return _RAW_STREAM(device.index)
     return torch.cuda.current_stream(device).cuda_stream
+
+
+_CURRENT_DEVICE = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _on_device(index: int, fn, *args) -> int:
+    """fn(*args) with device `index` as the current one: a stream's handle may
+    be 0, which means the current device's."""
+    if _CURRENT_DEVICE() == index:
+        return fn(*args)
+    with torch.cuda.device(index):
+        return fn(*args)
 
 
 def _require_gpu(*tensors: Optional[torch.Tensor]) -> torch.device:
@@ -488,3 +509,4 @@ def gather_qmm(x: torch.Tensor, w: torch.Tensor, scales: torch.Tensor,
 
 
 from .serving import KVCache, kv_append, paged_attention, sample  # noqa: E402  (needs the helpers above)
+from .pages import kv_compact, kv_fork, kv_free, kv_reserve  # noqa: E402

@@ -1,0 +1,461 @@
+// Bookkeeping of the cache's pages on the device: freeing, reserving, sharing
+// and compacting them.
+//
+// A page is free where refs, the number of table entries that name it, is not
+// above 0.  That number is the only state, so a result never depends on an
+// order: counts change by integer atomics, and pages are handed out by rank,
+// the lowest free one first, to entries in the order of (sequence, entry).
+//
+// Contents move as whole pages, copied for all layers' caches by one launch
+// whose pairs (from, to) the launch before it has left in the workspace.
+#include <algorithm>
+#include <climits>
+
+#include "kv_cache.hpp"
+#include "nvfp4_internal.hpp"
+
+namespace {
+
+using namespace nvfp4dev;
+
+constexpr int kThreads = 256;
+// Table cells of a block.
+constexpr int kCells = 4 * kThreads;
+// Threads of the block that plans, and pages that a thread looks at in a round.
+constexpr int kPlan = 1024, kScan = 16;
+// Bytes of a page's side that a block copies at a time, in 16-byte accesses.
+constexpr int kVecs = 4, kPiece = kVecs * kThreads * 16;
+// Caches of a copying launch: their addresses are its arguments.
+constexpr int kLayers = 32;
+// Copying blocks, eight a unit; more copies than that go round.
+constexpr int64_t kCopyBlocks = 2048;
+
+__device__ __forceinline__ bool is_page(int32_t id, int32_t pages) { return id >= 0 && id < pages; }
+
+// The sum of the threads' values before this one; *all gets the whole sum.
+__device__ __forceinline__ int block_scan(int v, int* shared, int* all) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int x = v;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int y = __shfl_up(x, off, 64);
+    x += lane >= off ? y : 0;
+  }
+  if (lane == 63) shared[wave] = x;
+  __syncthreads();
+  int before = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < kPlan / 64; ++w) {
+    before += w < wave ? shared[w] : 0;
+    sum += shared[w];
+  }
+  __syncthreads();   // the next scan writes `shared` again
+  *all = sum;
+  return before + x - v;
+}
+
+// A bit for each of the pages p .. p + kScan - 1 that is free.
+__device__ __forceinline__ uint32_t free_pages(const int32_t* refs, int64_t p, int32_t pages, bool vec) {
+  int32_t r[kScan];
+  if (vec && p + kScan <= pages) {
+#pragma unroll
+    for (int i = 0; i < kScan / 4; ++i) {
+      const int4 x = *((const int4*)(refs + p) + i);
+      r[4 * i] = x.x; r[4 * i + 1] = x.y; r[4 * i + 2] = x.z; r[4 * i + 3] = x.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kScan; ++i) r[i] = p + i < pages ? refs[p + i] : 1;
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < kScan; ++i) m |= r[i] <= 0 ? 1u << i : 0u;
+  return m;
+}
+
+// ---------------------------------------------------------------------------
+// freeing and sharing: every cell of the table by itself
+// ---------------------------------------------------------------------------
+
+struct FreeArgs {
+  int32_t* table;
+  const int32_t* lens;
+  int32_t* refs;
+  int64_t keep, sinks;
+  int32_t cells, width, pages, page_shift;
+};
+
+__global__ __launch_bounds__(kThreads) void free_kernel(FreeArgs A) {
+#pragma unroll
+  for (int r = 0; r < kCells / kThreads; ++r) {
+    const int64_t c = (int64_t)blockIdx.x * kCells + r * kThreads + threadIdx.x;
+    if (c >= A.cells) return;
+    const int32_t b = (int32_t)c / A.width, i = (int32_t)c - b * A.width;
+    const int64_t len = A.lens[b], begin = (int64_t)i << A.page_shift, end = begin + (1 << A.page_shift);
+    if (begin < len && (A.keep <= 0 || end > len - A.keep || begin < A.sinks)) continue;
+    const int32_t id = A.table[c];
+    if (is_page(id, A.pages)) {
+      A.table[c] = -1;
+      atomicSub(&A.refs[id], 1);
+    }
+  }
+}
+
+struct ForkArgs {
+  const int32_t *table, *lens, *parent;
+  int32_t *refs, *table_out, *lens_out;
+  int32_t batch, rows, width, pages;
+  int64_t cells;   // of the larger table, and at least its rows
+};
+
+__global__ __launch_bounds__(kThreads) void fork_kernel(ForkArgs A) {
+#pragma unroll
+  for (int r = 0; r < kCells / kThreads; ++r) {
+    const int64_t c = (int64_t)blockIdx.x * kCells + r * kThreads + threadIdx.x;
+    if (c >= A.cells) return;
+    if (c < A.rows) {
+      const int32_t p = A.parent[c];
+      A.lens_out[c] = is_page(p, A.batch) ? A.lens[p] : 0;
+    }
+    if (A.width == 0) continue;
+    const int32_t b = (int32_t)c / A.width, i = (int32_t)c - b * A.width;
+    int32_t from = -1, to = -1;
+    if (b < A.batch) from = A.table[c];
+    if (b < A.rows) {
+      const int32_t p = A.parent[b];
+      if (is_page(p, A.batch)) to = A.table[(int64_t)p * A.width + i];
+      A.table_out[c] = to;
+    }
+    // what a row keeps counts as before
+    if (from == to) continue;
+    if (is_page(to, A.pages)) atomicAdd(&A.refs[to], 1);
+    if (is_page(from, A.pages)) atomicSub(&A.refs[from], 1);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// reserving: one block
+// ---------------------------------------------------------------------------
+//
+// An item is a page slot of a sequence's new tokens: sequence b has those from
+// (first row / page) + 2 b on (one each without offsets).  First every item's
+// need, and its rank among them; then as many free pages as are needed, by
+// rank; then the entries.  A sequence's items are served together or not at all.
+
+struct ReserveArgs {
+  SequenceView s;
+  int32_t *table, *refs, *missing;
+  int32_t* copies;    // their number, and from [4] on the pairs (from, to)
+  int32_t* ranks;     // [items + 1]: needs before an item
+  int32_t* fresh;     // [items]: the pages taken, from rank kPlan on
+  int32_t items, pages, page_shift;
+  bool vec;           // 16-byte loads of refs
+};
+
+__device__ __forceinline__ int first_item(const ReserveArgs& A, int b) {
+  return A.s.cu ? (sequence_row(A.s, b) >> A.page_shift) + 2 * b : b;
+}
+
+struct Item {
+  int32_t b;
+  int32_t old;        // what the entry holds
+  int64_t cell;       // of the table; -1: no entry of new tokens
+  bool partly;        // the page holds earlier tokens too
+};
+
+__device__ __forceinline__ Item item_of(const ReserveArgs& A, int e) {
+  Item it;
+  it.b = e;
+  it.cell = -1;
+  it.old = -1;
+  it.partly = false;
+  int slot = 0;
+  if (A.s.cu) {
+    int lo = 0, hi = A.s.batch - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first_item(A, mid) <= e) lo = mid; else hi = mid - 1;
+    }
+    it.b = lo;
+    slot = e - first_item(A, lo);
+  }
+  const Sequence s = sequence(A.s, it.b);
+  const int first = s.first, stop = s.first + s.count, from = first < 0 ? 0 : first;
+  const int64_t i = (int64_t)(from >> A.page_shift) + slot;
+  if (slot < 0 || s.count <= 0 || i >= A.s.width || (i << A.page_shift) >= stop) return it;
+  it.cell = (int64_t)it.b * A.s.width + i;
+  it.old = A.table[it.cell];
+  it.partly = (i << A.page_shift) < from;
+  return it;
+}
+
+__global__ __launch_bounds__(kPlan) void reserve_kernel(ReserveArgs A) {
+  __shared__ int shared[kPlan / 64];
+  __shared__ int32_t fresh[kPlan];
+  __shared__ int copies;
+  const int tid = threadIdx.x;
+  if (tid == 0) copies = 0;
+
+  // needs, and their ranks; the first round's stay in registers
+  Item mine;
+  int my_rank = 0, want = 0;
+  bool my_need = false;
+  for (int base = 0; base < A.items; base += kPlan) {
+    const int e = base + tid;
+    Item it;
+    bool need = false;
+    if (e < A.items) {
+      it = item_of(A, e);
+      need = it.cell >= 0 && (!is_page(it.old, A.pages) || A.refs[it.old] > 1);
+    }
+    int all;
+    const int rank = want + block_scan(need, shared, &all);
+    if (e < A.items) A.ranks[e] = rank;
+    if (base == 0) {
+      mine = it;
+      my_rank = rank;
+      my_need = need;
+    }
+    want += all;
+  }
+  if (tid == 0) A.ranks[A.items] = want;
+
+  // the first `want` free pages
+  int have = 0;
+  for (int64_t p0 = 0; p0 < A.pages && have < want; p0 += kPlan * kScan) {
+    const int64_t p = p0 + tid * kScan;
+    uint32_t m = free_pages(A.refs, p, A.pages, A.vec);
+    int all, rank = have + block_scan(__popc(m), shared, &all);
+    for (; m && rank < want; m &= m - 1, ++rank) {
+      const int32_t id = (int32_t)(p + __builtin_ctz(m));
+      if (rank < kPlan) fresh[rank] = id; else A.fresh[rank] = id;
+    }
+    have += all;
+  }
+  __syncthreads();
+
+  const bool enough = have >= want;
+  const auto needs_until = [&](int b) { return A.ranks[b < A.s.batch ? min(first_item(A, b), A.items) : A.items]; };
+  for (int base = 0; base < A.items; base += kPlan) {
+    const int e = base + tid;
+    if (e >= A.items) continue;
+    if (base > 0) {
+      my_rank = A.ranks[e];
+      my_need = A.ranks[e + 1] != my_rank;
+      if (my_need) mine = item_of(A, e);
+    }
+    if (!my_need || !(enough || needs_until(mine.b + 1) <= have)) continue;
+    const int32_t id = my_rank < kPlan ? fresh[my_rank] : A.fresh[my_rank];
+    A.table[mine.cell] = id;
+    A.refs[id] = 1;
+    if (is_page(mine.old, A.pages)) {   // needed though it is there: it is shared
+      atomicSub(&A.refs[mine.old], 1);
+      if (mine.partly) {
+        const int at = atomicAdd(&copies, 1);
+        A.copies[4 + 2 * at] = mine.old;
+        A.copies[5 + 2 * at] = id;
+      }
+    }
+  }
+  for (int b = tid; b < A.s.batch; b += kPlan) {
+    int lack = 0;
+    if (!enough) {
+      const int until = needs_until(b + 1);
+      lack = until <= have ? 0 : until - needs_until(b);
+    }
+    A.missing[b] = lack;
+  }
+  __syncthreads();
+  if (tid == 0) A.copies[0] = copies;
+}
+
+// ---------------------------------------------------------------------------
+// compacting: one block plans
+// ---------------------------------------------------------------------------
+
+struct CompactArgs {
+  int32_t *refs, *used, *where;
+  int32_t* copies;    // their number, and from [4] on the pairs (from, to)
+  int32_t pages;
+  bool vec;
+};
+
+__global__ __launch_bounds__(kPlan) void compact_kernel(CompactArgs A) {
+  __shared__ int shared[kPlan / 64];
+  const int tid = threadIdx.x;
+  constexpr int kRound = kPlan * kScan;
+  int used = 0;
+  for (int64_t p0 = 0; p0 < A.pages; p0 += kRound) {
+    const int64_t p = p0 + tid * kScan;
+    const int64_t n = p < A.pages ? (A.pages - p < kScan ? A.pages - p : kScan) : 0;
+    used += (int)n - __popc(free_pages(A.refs, p, A.pages, A.vec));
+  }
+  int all;
+  block_scan(used, shared, &all);
+  used = all;
+  // holes below `used` and pages in use from there on: the k-th of these goes to the k-th of those
+  int holes = 0, movers = 0;
+  for (int64_t p0 = 0; p0 < A.pages; p0 += kRound) {
+    const int64_t p = p0 + tid * kScan;
+    const uint32_t inside = p >= A.pages ? 0 : A.pages - p < kScan ? (1u << (A.pages - p)) - 1 : (1u << kScan) - 1;
+    const uint32_t low = p >= used ? 0 : used - p < kScan ? (1u << (used - p)) - 1 : (1u << kScan) - 1;
+    const uint32_t empty = free_pages(A.refs, p, A.pages, A.vec) & inside;
+    uint32_t hole = empty & low, mover = inside & ~empty & ~low;
+#pragma unroll
+    for (int i = 0; i < kScan; ++i)
+      if ((inside >> i) & 1) A.where[p + i] = (empty >> i) & 1 ? -1 : (int32_t)(p + i);
+    int sum;   // a round has at most 2^14 of each
+    const int before = block_scan(__popc(hole) | (__popc(mover) << 16), shared, &sum);
+    for (int k = holes + (before & 0xffff); hole; hole &= hole - 1, ++k) A.copies[5 + 2 * k] = (int32_t)(p + __builtin_ctz(hole));
+    for (int k = movers + (before >> 16); mover; mover &= mover - 1, ++k) A.copies[4 + 2 * k] = (int32_t)(p + __builtin_ctz(mover));
+    holes += sum & 0xffff;
+    movers += sum >> 16;
+  }
+  __syncthreads();
+  for (int k = tid; k < movers; k += kPlan) {
+    const int32_t from = A.copies[4 + 2 * k], to = A.copies[5 + 2 * k];
+    A.where[from] = to;
+    A.refs[to] = A.refs[from];
+    A.refs[from] = 0;
+  }
+  if (tid == 0) {
+    A.copies[0] = movers;
+    *A.used = used;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// copying
+// ---------------------------------------------------------------------------
+
+struct CopyArgs {
+  const int32_t* copies;
+  int64_t page_bytes;       // of a side
+  int32_t heads, layers, pieces;
+  int32_t table_blocks;     // blocks before the copying ones that rewrite the table
+  int32_t* table;
+  const int32_t* where;
+  int32_t cells, pages;
+  uint8_t *k[kLayers], *v[kLayers], *ks[kLayers], *vs[kLayers];
+};
+
+__global__ __launch_bounds__(kThreads) void copy_kernel(CopyArgs A) {
+  if ((int)blockIdx.x < A.table_blocks) {
+#pragma unroll
+    for (int r = 0; r < kCells / kThreads; ++r) {
+      const int64_t c = (int64_t)blockIdx.x * kCells + r * kThreads + threadIdx.x;
+      if (c >= A.cells) return;
+      const int32_t id = A.table[c];
+      if (is_page(id, A.pages)) A.table[c] = A.where[id];
+    }
+    return;
+  }
+  const int64_t all = (int64_t)A.copies[0] * A.layers * 2 * A.pieces, step = gridDim.x - A.table_blocks;
+  for (int64_t at = blockIdx.x - A.table_blocks; at < all; at += step) {
+    int64_t rest = at;
+    const int piece = (int)(rest % A.pieces);
+    rest /= A.pieces;
+    const int side = (int)(rest & 1);
+    rest >>= 1;
+    const int layer = (int)(rest % A.layers);
+    const int64_t pair = rest / A.layers;
+    const int64_t from = A.copies[4 + 2 * pair], to = A.copies[5 + 2 * pair];
+    uint8_t* base = side ? A.v[layer] : A.k[layer];
+    const uint4* src = (const uint4*)(base + from * A.page_bytes);
+    uint4* dst = (uint4*)(base + to * A.page_bytes);
+    const int64_t vecs = A.page_bytes / 16, first = (int64_t)piece * (kPiece / 16) + threadIdx.x;
+    uint4 x[kVecs];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+      if (first + i * kThreads < vecs) x[i] = src[first + i * kThreads];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+      if (first + i * kThreads < vecs) dst[first + i * kThreads] = x[i];
+    if (piece == 0) {
+      uint8_t* scales = side ? A.vs[layer] : A.ks[layer];
+      for (int h = threadIdx.x; h < A.heads; h += kThreads) scales[to * A.heads + h] = scales[from * A.heads + h];
+    }
+  }
+}
+
+int64_t blocks_of(int64_t cells) { return (cells + kCells - 1) / kCells; }
+
+void launch_copies(const nvfp4_kv_cache_t* caches, int64_t count, const int32_t* copies, int64_t most, int32_t* table,
+                   const int32_t* where, int64_t cells, hipStream_t s) {
+  CopyArgs A;
+  A.copies = copies;
+  A.page_bytes = caches->heads * caches->page * caches->dim;
+  A.heads = (int32_t)caches->heads;
+  A.pages = (int32_t)caches->pages;
+  A.pieces = (int32_t)((A.page_bytes + kPiece - 1) / kPiece);
+  A.table = table;
+  A.where = where;
+  A.cells = (int32_t)cells;
+  for (int64_t at = 0; at < count; at += kLayers) {
+    A.layers = (int32_t)std::min<int64_t>(kLayers, count - at);
+    A.table_blocks = at == 0 && table ? (int32_t)blocks_of(cells) : 0;
+    for (int i = 0; i < kLayers; ++i) {
+      const nvfp4_kv_cache_t& c = caches[at + (i < A.layers ? i : 0)];
+      A.k[i] = c.k; A.v[i] = c.v; A.ks[i] = c.k_scales; A.vs[i] = c.v_scales;
+    }
+    int64_t copying = kCopyBlocks;
+    if (most < kCopyBlocks) copying = std::min(copying, most * A.layers * 2 * std::min<int64_t>(A.pieces, kCopyBlocks));
+    const int64_t blocks = A.table_blocks + copying;
+    if (blocks > 0) copy_kernel<<<dim3((uint32_t)blocks), dim3(kThreads), 0, s>>>(A);
+  }
+}
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+}  // namespace
+
+namespace nvfp4host {
+
+int64_t kv_reserve_items(int64_t tokens, int64_t batch, int64_t page, bool offsets) {
+  return offsets ? tokens / page + 2 * batch : batch;
+}
+
+int64_t kv_reserve_bytes(int64_t items, int64_t batch) { return ((4 + 2 * batch + 2 * items + 1) * 4 + 255) / 256 * 256; }
+
+int64_t kv_compact_bytes(int64_t pages) { return ((4 + pages + 1) * 4 + 255) / 256 * 256; }
+
+void launch_kv_free(int32_t* table, int64_t batch, int64_t width, const int32_t* lens, int64_t page, int64_t keep,
+                    int64_t sinks, int32_t* refs, int64_t pages, hipStream_t s) {
+  const FreeArgs A = {table, lens, refs, keep, sinks, (int32_t)(batch * width), (int32_t)width, (int32_t)pages,
+                      __builtin_ctz((unsigned)page)};
+  free_kernel<<<dim3((uint32_t)blocks_of(A.cells)), dim3(kThreads), 0, s>>>(A);
+}
+
+void launch_kv_fork(const int32_t* table, int64_t batch, int64_t width, const int32_t* lens, const int32_t* parent,
+                    int64_t rows, int32_t* refs, int64_t pages, int32_t* table_out, int32_t* lens_out, hipStream_t s) {
+  const int64_t cells = std::max(std::max(batch, rows) * width, rows);
+  const ForkArgs A = {table, lens, parent, refs, table_out, lens_out, (int32_t)batch, (int32_t)rows, (int32_t)width,
+                      (int32_t)pages, cells};
+  fork_kernel<<<dim3((uint32_t)blocks_of(cells)), dim3(kThreads), 0, s>>>(A);
+}
+
+void launch_kv_reserve(const nvfp4_kv_cache_t* caches, int64_t count, int32_t* table, int64_t batch, int64_t width,
+                       const int32_t* lens, const int32_t* cu, int64_t tokens, int32_t* refs, void* ws,
+                       int32_t* missing, hipStream_t s) {
+  ReserveArgs A;
+  const int64_t items = kv_reserve_items(tokens, batch, caches->page, cu != nullptr);
+  A.s = {table, lens, cu, width, (int32_t)batch, (int32_t)tokens, INT_MAX};
+  A.table = table; A.refs = refs; A.missing = missing;
+  A.copies = (int32_t*)ws;
+  A.ranks = A.copies + 4 + 2 * batch;
+  A.fresh = A.ranks + items + 1;
+  A.items = (int32_t)items; A.pages = (int32_t)caches->pages;
+  A.page_shift = __builtin_ctz((unsigned)caches->page);
+  A.vec = aligned16(refs);
+  reserve_kernel<<<dim3(1), dim3(kPlan), 0, s>>>(A);
+  launch_copies(caches, count, A.copies, batch, nullptr, nullptr, 0, s);
+}
+
+void launch_kv_compact(const nvfp4_kv_cache_t* caches, int64_t count, int32_t* table, int64_t batch, int64_t width,
+                       int32_t* refs, void* ws, int32_t* used, int32_t* where, hipStream_t s) {
+  const CompactArgs A = {refs, used, where, (int32_t*)ws, (int32_t)caches->pages, aligned16(refs)};
+  compact_kernel<<<dim3(1), dim3(kPlan), 0, s>>>(A);
+  launch_copies(caches, count, A.copies, caches->pages / 2, table, where, batch * width, s);
+}
+
+}  // namespace nvfp4host

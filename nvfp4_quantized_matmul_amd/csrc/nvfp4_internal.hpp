@@ -145,6 +145,20 @@ void launch_paged_attention(const nvfp4_kv_cache_t& c, const void* q, int64_t q_
                             nvfp4_dtype_t dt, int64_t tokens, const int32_t* cu, int64_t batch, int64_t max_q,
                             const int32_t* table, int64_t width, const int32_t* lens, int64_t window, float scale,
                             void* ws, int64_t ws_bytes, void* out, hipStream_t s);
+// The pages' bookkeeping.  kv_reserve_items: page slots that new tokens may
+// reach.
+int64_t kv_reserve_items(int64_t tokens, int64_t batch, int64_t page, bool offsets);
+int64_t kv_reserve_bytes(int64_t items, int64_t batch);
+int64_t kv_compact_bytes(int64_t pages);
+void launch_kv_free(int32_t* table, int64_t batch, int64_t width, const int32_t* lens, int64_t page, int64_t keep,
+                    int64_t sinks, int32_t* refs, int64_t pages, hipStream_t s);
+void launch_kv_fork(const int32_t* table, int64_t batch, int64_t width, const int32_t* lens, const int32_t* parent,
+                    int64_t rows, int32_t* refs, int64_t pages, int32_t* table_out, int32_t* lens_out, hipStream_t s);
+void launch_kv_reserve(const nvfp4_kv_cache_t* caches, int64_t count, int32_t* table, int64_t batch, int64_t width,
+                       const int32_t* lens, const int32_t* cu, int64_t tokens, int32_t* refs, void* ws,
+                       int32_t* missing, hipStream_t s);
+void launch_kv_compact(const nvfp4_kv_cache_t* caches, int64_t count, int32_t* table, int64_t batch, int64_t width,
+                       int32_t* refs, void* ws, int32_t* used, int32_t* where, hipStream_t s);
 // One token per row of logits; sample_bytes is the workspace with which
 // several blocks share a row (0: none).
 int64_t sample_bytes(int64_t batch, int64_t vocab, nvfp4_dtype_t dt);

@@ -1,9 +1,10 @@
-// C ABI of the serving operators (cache append, paged attention, sampling):
-// argument checks and launches.  Every check runs on the host before anything
+// C ABI of the serving operators (cache append, paged attention, pages,
+// sampling): argument checks and launches.  Every check runs on the host before anything
 // is enqueued; sequence lengths, row offsets and page tables live on the
 // device and are bounded by the kernels.
 #include <climits>
 #include <cstdint>
+#include <initializer_list>
 
 #include "nvfp4_internal.hpp"
 
@@ -75,6 +76,42 @@ int check_sequences(const int32_t* cu_q, int64_t tokens, int64_t batch, const in
   if (!lens || (width > 0 && !table)) return NVFP4_ERR_NULLPTR;
   if (!aligned(lens, 4) || !aligned(table, 4) || !aligned(cu_q, 4)) return NVFP4_ERR_ALIGN;
   return NVFP4_OK;
+}
+
+// The layers' caches: one geometry.
+int check_caches(const nvfp4_kv_cache_t* c, int64_t count) {
+  if (!c) return NVFP4_ERR_NULLPTR;
+  if (count < 1) return NVFP4_ERR_SHAPE;
+  for (int64_t i = 0; i < count; ++i) {
+    int64_t bytes;
+    const int st = check_cache(c + i, &bytes);
+    if (st != NVFP4_OK) return st;
+    if (c[i].pages != c->pages || c[i].heads != c->heads || c[i].page != c->page || c[i].dim != c->dim)
+      return NVFP4_ERR_SHAPE;
+  }
+  return NVFP4_OK;
+}
+
+int check_table(const int32_t* table, int64_t batch, int64_t width, const int32_t* refs, int64_t pages) {
+  int64_t cells;
+  if (batch < 0 || width < 0 || pages < 0) return NVFP4_ERR_SHAPE;
+  if (batch > INT_MAX || width > INT_MAX || pages > INT_MAX || !mul_ok(batch, width, &cells) || cells > INT_MAX)
+    return NVFP4_ERR_SHAPE;
+  if ((cells > 0 && !table) || (pages > 0 && !refs)) return NVFP4_ERR_NULLPTR;
+  if (!aligned(table, 4) || !aligned(refs, 4)) return NVFP4_ERR_ALIGN;
+  return NVFP4_OK;
+}
+
+// Whether any two of the int32 arrays (address, length) overlap.
+struct Ints {
+  const void* p;
+  int64_t n;
+};
+bool any_overlap(std::initializer_list<Ints> arrays) {
+  for (const Ints* a = arrays.begin(); a != arrays.end(); ++a)
+    for (const Ints* b = arrays.begin(); b != a; ++b)
+      if (a->p && b->p && a->n > 0 && b->n > 0 && overlaps(a->p, a->n * 4, b->p, b->n * 4)) return true;
+  return false;
 }
 
 }  // namespace
@@ -173,6 +210,98 @@ int nvfp4_paged_attention(const nvfp4_kv_cache_t* cache, const void* q, int64_t 
     return NVFP4_ERR_GRID;
   nvfp4host::launch_paged_attention(*cache, q, q_token, q_head, heads_q, dtype, tokens, cu_q, batch, max_q, table,
                                     table_width, lens, window, scale, workspace, workspace_bytes, out, stream);
+  return launched();
+}
+
+int nvfp4_kv_free(int32_t* table, int64_t batch, int64_t width, const int32_t* lens, int64_t page, int64_t keep,
+                  int64_t sinks, int32_t* refs, int64_t pages, hipStream_t stream) {
+  int st = check_page(page, 64);
+  if (st != NVFP4_OK) return st;
+  st = check_table(table, batch, width, refs, pages);
+  if (st != NVFP4_OK) return st;
+  int64_t t;
+  if (!mul_ok(width, page, &t) || t > kMaxPositions) return NVFP4_ERR_SHAPE;
+  if (batch == 0 || width == 0) return NVFP4_OK;
+  if (!lens) return NVFP4_ERR_NULLPTR;
+  if (!aligned(lens, 4)) return NVFP4_ERR_ALIGN;
+  if (any_overlap({{table, batch * width}, {refs, pages}, {lens, batch}})) return NVFP4_ERR_SHAPE;
+  // more than any length: all of it is kept
+  if (keep > INT_MAX) keep = 0;
+  nvfp4host::launch_kv_free(table, batch, width, lens, page, keep, sinks, refs, pages, stream);
+  return launched();
+}
+
+int64_t nvfp4_kv_reserve_workspace_size(int64_t tokens, int64_t batch, int64_t page) {
+  const int st = check_page(page, 64);
+  if (st != NVFP4_OK) return st;
+  if (tokens < 0 || batch < 0 || tokens > INT_MAX || batch > kMaxPositions) return NVFP4_ERR_SHAPE;
+  const int64_t items = nvfp4host::kv_reserve_items(tokens, batch, page, true);
+  if (items > INT_MAX) return NVFP4_ERR_SHAPE;
+  return batch == 0 ? 0 : nvfp4host::kv_reserve_bytes(items, batch);
+}
+
+int nvfp4_kv_reserve(const nvfp4_kv_cache_t* caches, int64_t count, int32_t* table, int64_t batch, int64_t width,
+                     const int32_t* lens, const int32_t* cu_q, int64_t tokens, int32_t* refs, void* workspace,
+                     int64_t workspace_bytes, int32_t* missing, hipStream_t stream) {
+  int st = check_caches(caches, count);
+  if (st != NVFP4_OK) return st;
+  const int64_t pages = caches->pages;
+  st = check_table(table, batch, width, refs, pages);
+  if (st != NVFP4_OK) return st;
+  const int64_t need = nvfp4_kv_reserve_workspace_size(tokens, batch, caches->page);
+  if (need < 0) return (int)need;
+  int64_t t;
+  if (!mul_ok(width, caches->page, &t) || t > kMaxPositions) return NVFP4_ERR_SHAPE;
+  if (batch == 0) return tokens == 0 || cu_q ? NVFP4_OK : NVFP4_ERR_SHAPE;
+  st = check_sequences(cu_q, tokens, batch, table, width, lens);
+  if (st != NVFP4_OK) return st;
+  if (!missing || !workspace) return NVFP4_ERR_NULLPTR;
+  if (!aligned(missing, 4) || !aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
+  if (workspace_bytes < need) return NVFP4_ERR_SHAPE;
+  if (any_overlap({{table, batch * width}, {refs, pages}, {lens, batch}, {cu_q, batch + 1}, {missing, batch}, {workspace, need / 4}}))
+    return NVFP4_ERR_SHAPE;
+  nvfp4host::launch_kv_reserve(caches, count, table, batch, width, lens, cu_q, tokens, refs, workspace, missing, stream);
+  return launched();
+}
+
+int nvfp4_kv_fork(const int32_t* table, int64_t batch, int64_t width, const int32_t* lens, const int32_t* parent,
+                  int64_t rows, int32_t* refs, int64_t pages, int32_t* table_out, int32_t* lens_out,
+                  hipStream_t stream) {
+  int st = check_table(table, batch, width, refs, pages);
+  if (st != NVFP4_OK) return st;
+  int64_t cells;
+  if (rows < 0 || rows > INT_MAX || !mul_ok(rows, width, &cells) || cells > INT_MAX) return NVFP4_ERR_SHAPE;
+  if (rows == 0 && (batch == 0 || width == 0)) return NVFP4_OK;
+  if ((batch > 0 && !lens) || (rows > 0 && (!parent || !lens_out)) || (cells > 0 && !table_out)) return NVFP4_ERR_NULLPTR;
+  if (!aligned(lens, 4) || !aligned(parent, 4) || !aligned(table_out, 4) || !aligned(lens_out, 4)) return NVFP4_ERR_ALIGN;
+  // lengths and parents are only read, so these may be one array
+  if (any_overlap({{table, batch * width}, {refs, pages}, {table_out, cells}, {lens_out, rows}, {lens, batch}}) ||
+      any_overlap({{refs, pages}, {table_out, cells}, {lens_out, rows}, {parent, rows}}))
+    return NVFP4_ERR_SHAPE;
+  nvfp4host::launch_kv_fork(table, batch, width, lens, parent, rows, refs, pages, table_out, lens_out, stream);
+  return launched();
+}
+
+int64_t nvfp4_kv_compact_workspace_size(int64_t pages) {
+  if (pages < 0 || pages > INT_MAX) return NVFP4_ERR_SHAPE;
+  return nvfp4host::kv_compact_bytes(pages);
+}
+
+int nvfp4_kv_compact(const nvfp4_kv_cache_t* caches, int64_t count, int32_t* table, int64_t batch, int64_t width,
+                     int32_t* refs, void* workspace, int64_t workspace_bytes, int32_t* used, int32_t* where,
+                     hipStream_t stream) {
+  int st = check_caches(caches, count);
+  if (st != NVFP4_OK) return st;
+  const int64_t pages = caches->pages;
+  st = check_table(table, batch, width, refs, pages);
+  if (st != NVFP4_OK) return st;
+  const int64_t cells = batch * width;
+  const int64_t need = nvfp4_kv_compact_workspace_size(pages);
+  if (!used || !workspace || (pages > 0 && !where)) return NVFP4_ERR_NULLPTR;
+  if (!aligned(used, 4) || !aligned(where, 4) || !aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
+  if (workspace_bytes < need) return NVFP4_ERR_SHAPE;
+  if (any_overlap({{table, cells}, {refs, pages}, {used, 1}, {where, pages}, {workspace, need / 4}})) return NVFP4_ERR_SHAPE;
+  nvfp4host::launch_kv_compact(caches, count, table, batch, width, refs, workspace, used, where, stream);
   return launched();
 }
 
