@@ -509,6 +509,22 @@ int nvfp4_paged_attention(const nvfp4_kv_cache_t* cache, const void* q, int64_t 
                           int64_t workspace_bytes, void* out, hipStream_t stream);
 
 /*
+ * nvfp4_paged_attention_sinks -- nvfp4_paged_attention whose queries see,
+ * besides their window, the first `sinks` tokens of their sequence: the query
+ * of position p sees the tokens t <= p with t > p - window or t < sinks.  With
+ * sinks <= 0 or window <= 0 it is nvfp4_paged_attention.  Pages that no query
+ * of the call sees are not read and need not be there.
+ */
+int64_t nvfp4_paged_attention_sinks_workspace_size(int64_t tokens, int64_t heads_q, int64_t heads, int64_t dim,
+                                                   int64_t page, int64_t batch, int64_t max_q, int64_t table_width,
+                                                   int64_t window, int64_t sinks, nvfp4_dtype_t dtype);
+int nvfp4_paged_attention_sinks(const nvfp4_kv_cache_t* cache, const void* q, int64_t q_token, int64_t q_head,
+                                int64_t heads_q, nvfp4_dtype_t dtype, int64_t tokens, const int32_t* cu_q,
+                                int64_t batch, int64_t max_q, const int32_t* table, int64_t table_width,
+                                const int32_t* lens, int64_t window, int64_t sinks, float scale, void* workspace,
+                                int64_t workspace_bytes, void* out, hipStream_t stream);
+
+/*
  * Pages of the cache, kept on the device: which of them are free, which ones a
  * sequence has, and sequences that share theirs.  The caches of all layers
  * (nvfp4_kv_cache_t caches[count], of one geometry) go by one table and one

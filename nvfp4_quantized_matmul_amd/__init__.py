@@ -86,6 +86,9 @@ def load_library() -> ctypes.CDLL:
         "nvfp4_paged_attention_workspace_size": [i64] * 9 + [c_int],
         "nvfp4_paged_attention": [vp, vp, i64, i64, i64, c_int, i64, vp, i64, i64, vp, i64, vp, i64, ctypes.c_float,
                                   vp, i64, vp, vp],
+        "nvfp4_paged_attention_sinks_workspace_size": [i64] * 10 + [c_int],
+        "nvfp4_paged_attention_sinks": [vp, vp, i64, i64, i64, c_int, i64, vp, i64, i64, vp, i64, vp, i64, i64,
+                                        ctypes.c_float, vp, i64, vp, vp],
         "nvfp4_sample_workspace_size": [i64, i64, c_int],
         "nvfp4_sample": [vp, c_int, i64, i64, i64, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp],
         "nvfp4_kv_free": [vp, i64, i64, vp, i64, i64, i64, vp, i64, vp],
@@ -108,6 +111,7 @@ def load_library() -> ctypes.CDLL:
     lib.nvfp4_qmm_glu_workspace_size.restype = i64
     lib.nvfp4_static_scratch_bytes.restype = i64
     lib.nvfp4_paged_attention_workspace_size.restype = i64
+    lib.nvfp4_paged_attention_sinks_workspace_size.restype = i64
     lib.nvfp4_sample_workspace_size.restype = i64
     lib.nvfp4_kv_reserve_workspace_size.restype = i64
     lib.nvfp4_kv_compact_workspace_size.restype = i64

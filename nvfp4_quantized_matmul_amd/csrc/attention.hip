@@ -41,6 +41,7 @@ struct AttnArgs {
   float *part_o, *part_m, *part_l;   // of a split axis: [tokens * heads_q][splits][dim], twice [tokens * heads_q][splits]
   int32_t heads_q, group;
   int32_t window;                    // <= 0: none
+  int32_t sinks;                     // first tokens that are seen through any window
   int32_t splits, chunk;             // chunk: tokens of a split, a multiple of 64
   int32_t row_tiles;                 // of a sequence and head, at most
   float scale_log2;                  // |scale| * log2(e)
@@ -205,6 +206,7 @@ __device__ __forceinline__ float sum_across_groups(float v) {
 struct Span {
   int32_t first, last;   // positions of the first and the last row
   int32_t begin, end;    // cached tokens that any of the rows sees; begin on a tile
+  int32_t from;          // where the window's part of them starts
 };
 
 // The first position that a row at position p sees through the window.
@@ -220,9 +222,22 @@ __device__ __forceinline__ Span span_of(const AttnArgs& A, const Sequence& s, in
   r.end = r.last + 1 < cap ? r.last + 1 : (int32_t)cap;
   const int32_t lo = first_seen(A, r.first);
   // behind the table there is nothing, and positions from there on would pass 32 bits
-  r.begin = (lo < cap ? lo : (int32_t)cap) & ~63;
+  r.from = (lo < cap ? lo : (int32_t)cap) & ~63;
+  // Sinks: their tiles come right before the window's part, so that what goes
+  // along the axis and splits it sees one axis [begin, end); see place_of.
+  const int32_t front = A.sinks < r.from ? A.sinks : r.from;
+  r.begin = r.from - ((front + 63) & ~63);
   return r;
 }
+
+// The token at place t of the axis.
+template <bool SINKS>
+__device__ __forceinline__ int place_of(const Span& sp, int t) { return SINKS && t < sp.from ? t - sp.begin : t; }
+
+// Whether rows whose windows start at `from` or before see the tile at token t0
+// whole, as far as window and sinks go.
+template <bool SINKS>
+__device__ __forceinline__ bool in_reach(const AttnArgs& A, int t0, int from) { return t0 >= from || (SINKS && t0 + 64 <= A.sinks); }
 
 // ---------------------------------------------------------------------------
 // Few rows: the waves of a block share the rows and split the tokens
@@ -259,7 +274,7 @@ constexpr int few_lds_bytes() {
 template <int DIM, int NT, int PARTS>
 constexpr int few_blocks_per_cu() { return NT * DIM / 4 + 16 * NT + DIM / 2 + 24 * PARTS * NT + 64 <= 256 ? 2 : 1; }
 
-template <typename T, int DIM, int NT>
+template <typename T, int DIM, int NT, bool SINKS>
 __global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>::kParts>())) void few_rows_kernel(AttnArgs A) {
   typedef Mma<T> M;
   typedef typename M::V8 V8;
@@ -334,7 +349,7 @@ __global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>:
   // that it means there; -1 where there is none.  Entries are fetched a tile
   // ahead and no load stands behind a branch: waiting for either at once would
   // wait for every load of codes before it.
-  auto entry_of = [&](int t) -> int { return table[(t < hi ? t : hi - 1) >> shift]; };
+  auto entry_of = [&](int t) -> int { return table[place_of<SINKS>(sp, t < hi ? t : hi - 1) >> shift]; };
   auto page_of = [&](int entry, int t) -> int { return entry < A.c.pages && t < hi ? entry : -1; };
 
   constexpr int STEP = 64 * kFewWaves;
@@ -368,15 +383,15 @@ __global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>:
     idv = page_of(entry_of(t0 + tv), t0 + tv);
     entry_k = entry_of(t0 + STEP + tk);
     entry_v = entry_of(t0 + STEP + tv);
-    load_k(t0, idk);
-    load_v(t0, idv);
+    load_k(place_of<SINKS>(sp, t0), idk);
+    load_v(place_of<SINKS>(sp, t0), idv);
   }
   for (; t0 < hi; t0 += STEP) {
     const int t_next = t0 + STEP;
     asm volatile("" ::: "memory");   // the query operands are read from LDS in each tile: held, they would fill the registers
     // behind the last tile that one is loaded again
     const bool more = t_next < hi;
-    const int t_load = more ? t_next : t0;
+    const int t_load = place_of<SINKS>(sp, more ? t_next : t0), at = place_of<SINKS>(sp, t0);
     const int idk_next = more ? page_of(entry_k, t_next + tk) : idk, idv_next = more ? page_of(entry_v, t_next + tv) : idv;
     entry_k = entry_of(t_next + STEP + tk);
     entry_v = entry_of(t_next + STEP + tv);
@@ -409,7 +424,7 @@ __global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>:
     load_k(t_load, idk_next);
 
     // what each row sees; a tile that all rows see whole needs no comparison
-    const bool whole = t0 + 63 <= sp.first && t0 >= from_last && t0 + 64 <= hi &&
+    const bool whole = at + 63 <= sp.first && in_reach<SINKS>(A, at, from_last) && t0 + 64 <= hi &&
                        __all(idv >= 0);   // columns without a row may hold anything
     V8 pw[NT][2][PARTS];
     uint32_t seen[NT];
@@ -418,13 +433,13 @@ __global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>:
       seen[nt] = 0xffffu;
       if (!whole) {
         seen[nt] = 0;
-        const int tg = t0 + 16 * g;
+        const int tg = at + 16 * g;
         // tokens tg + i with i <= last_i and i >= first_i
         const int last_i = (pos[nt] < hi ? pos[nt] : hi - 1) - tg;
-        const int first_i = first_seen(A, pos[nt]) - tg;
+        const int first_i = first_seen(A, pos[nt]) - tg, sinks_i = A.sinks - tg;
         if (idv >= 0) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) seen[nt] |= (i <= last_i && i >= first_i) ? 1u << i : 0u;
+          for (int i = 0; i < 16; ++i) seen[nt] |= (i <= last_i && (i >= first_i || (SINKS && i < sinks_i))) ? 1u << i : 0u;
         }
       }
       // a lane's tokens share their scales: of a tile that is seen whole only
@@ -692,7 +707,7 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-template <typename T, int DIM, bool ONE_PAGE>
+template <typename T, int DIM, bool ONE_PAGE, bool SINKS>
 __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1) void many_rows_kernel(AttnArgs A) {
   typedef typename Mma<T>::V8 V8;
   typedef typename Mma<T>::E E;
@@ -776,7 +791,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1
 #pragma unroll
     for (int i = 0; i < IDS; ++i) {
       const int t = token(t0, i);
-      int at = (t < hi ? t : hi - 1) >> shift;
+      int at = place_of<SINKS>(sp, t < hi ? t : hi - 1) >> shift;
       asm("" : "+v"(at));
       entry[i] = table[at];
     }
@@ -788,7 +803,8 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1
       if constexpr (ONE_PAGE) id[i] = __builtin_amdgcn_readfirstlane(id[i]);
     }
   };
-  auto load = [&](int t0) {
+  auto load = [&](int place) {
+    const int t0 = place_of<SINKS>(sp, place);
 #pragma unroll
     for (int i = 0; i < KLOADS; ++i) {
       if constexpr (ONE_PAGE) {
@@ -856,8 +872,9 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1
   float m = -__builtin_inff(), l = 0.0f;
 
   // a tile is partial for the block if a row does not see it whole or a page is missing
-  auto partial = [&](int t0) -> bool {
-    return t0 + 63 > sp.first || t0 < from_last || t0 + 64 > hi || __any(id[VALUES] < 0);
+  auto partial = [&](int place) -> bool {
+    const int t0 = place_of<SINKS>(sp, place);
+    return t0 + 63 > sp.first || !in_reach<SINKS>(A, t0, from_last) || place + 64 > hi || __any(id[VALUES] < 0);
   };
 
   if (tid < 2) S.nan[tid] = -1;
@@ -872,12 +889,13 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1
     ids(lo + 64);
     fetch_ids(lo + 128);
   }
-  for (int t0 = lo; t0 < hi; t0 += 64, at ^= 1) {
+  for (int place = lo; place < hi; place += 64, at ^= 1) {
     lds_barrier();
-    load(t0 + 64);   // also behind the last tile, from page 0
-    const bool next_partial = partial(t0 + 64);
+    load(place + 64);   // also behind the last tile, from page 0
+    const bool next_partial = partial(place + 64);
+    const int t0 = place_of<SINKS>(sp, place);
     const ManyTile<DIM>& t = S.tile[at];
-    const bool unseen = t0 > wlast || t0 + 63 < from_wfirst;
+    const bool unseen = t0 > wlast || (t0 + 63 < from_wfirst && !(SINKS && t0 < A.sinks));
     if (!unseen) {
       f32x16_t sc[2];
 #pragma unroll
@@ -893,7 +911,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1
         }
       }
       const uint32_t there = S.there[at];
-      const bool whole = t0 + 63 <= wfirst && t0 >= from_wlast && wave_rows == 32 && there == 0xfu;
+      const bool whole = t0 + 63 <= wfirst && in_reach<SINKS>(A, t0, from_wlast) && wave_rows == 32 && there == 0xfu;
       // the largest score, and the factor and summand that make weights of
       // scores: of tiles that are seen whole only the largest of each group of
       // 16 tokens is scaled for it (the factors are not negative)
@@ -919,7 +937,13 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1
         top = -__builtin_inff();
         const int last_i = pos - t0, first_i = first_seen(A, pos) - t0;
         vis = last_i < 0 ? 0 : last_i >= 63 ? ~0ull : (2ull << last_i) - 1;
-        if (first_i > 0) vis = first_i > 63 ? 0 : vis & (~0ull << first_i);
+        if constexpr (SINKS) {
+          const int sinks_i = A.sinks - t0;
+          const uint64_t sinks = sinks_i <= 0 ? 0 : sinks_i >= 64 ? ~0ull : (1ull << sinks_i) - 1;
+          vis &= sinks | (first_i > 63 ? 0 : first_i > 0 ? ~0ull << first_i : ~0ull);
+        } else if (first_i > 0) {
+          vis = first_i > 63 ? 0 : vis & (~0ull << first_i);
+        }
 #pragma unroll
         for (int g = 0; g < 4; ++g) vis &= (there >> g) & 1 ? ~0ull : ~(0xffffull << (16 * g));
         const uint32_t seen[2] = {(uint32_t)vis >> (8 * hh), (uint32_t)(vis >> 32) >> (8 * hh)};
@@ -978,7 +1002,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1
           const int ch = 32 * c + n;
           o[c] = Mma32<T>::mul(__builtin_bit_cast(V8, t.v[ch * 8 + ((2 * g + hh) ^ swizzle<8>(ch))]), pw[g], o[c]);
         }
-      if (S.nan[at] == t0) {
+      if (S.nan[at] == place) {
         // NaN codes lie as zeros in the tile: a channel with one that the row sees is NaN
 #pragma unroll
         for (int c = 0; c < CB; ++c)
@@ -989,9 +1013,9 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1
           }
       }
     }
-    store(at ^ 1, t0 + 64, next_partial);   // its readers have passed this round's barrier
-    ids(t0 + 128);
-    fetch_ids(t0 + 192);
+    store(at ^ 1, place + 64, next_partial);   // its readers have passed this round's barrier
+    ids(place + 128);
+    fetch_ids(place + 192);
   }
 
   l += __shfl_xor(l, 32, 64);
@@ -1107,7 +1131,7 @@ struct Plan {
 };
 
 Plan make_plan(int64_t heads_q, int64_t heads, int64_t page, int64_t batch, int64_t max_q, int64_t width,
-               int64_t window, nvfp4_dtype_t dt, int64_t dim, bool split) {
+               int64_t window, int64_t sinks, nvfp4_dtype_t dt, int64_t dim, bool split) {
   Plan p;
   const int64_t group = heads_q / heads, rows = max_q * group;
   p.many = dt != NVFP4_F32 && rows > 32;
@@ -1117,7 +1141,8 @@ Plan make_plan(int64_t heads_q, int64_t heads, int64_t page, int64_t batch, int6
   // the longest span of a tile of rows, from a tile boundary on
   int64_t span = width * page;
   if (window > 0 && window < span) {
-    const int64_t w = window - 1 + (p.rows + group - 1) / group + 1 + 63;
+    const int64_t front = sinks <= 0 ? 0 : sinks < span ? (sinks + 63) / 64 * 64 : span;
+    const int64_t w = window - 1 + (p.rows + group - 1) / group + 1 + 63 + front;
     if (w < span) span = w;
   }
   const int64_t tiles = (span + 63) / 64, base = batch * heads * p.row_tiles;   // max_q * heads_q is at most 2^30
@@ -1147,35 +1172,40 @@ int64_t partials(const Plan& p, int64_t tokens, int64_t heads_q, int64_t dim) {
   return p.splits > 1 ? tokens * heads_q * p.splits * (dim + 2) * 4 : 0;
 }
 
-template <typename T, int DIM, int NT>
+template <typename T, int DIM, int NT, bool SINKS>
 bool launch_few(const AttnArgs& A, int64_t blocks, hipStream_t s) {
   constexpr int bytes = few_lds_bytes<DIM, NT, Mma<T>::kParts>();
   static_assert(bytes <= 160 * 1024, "LDS of a workgroup");
   if constexpr (bytes > 64 * 1024) {
-    if (hipFuncSetAttribute((const void*)few_rows_kernel<T, DIM, NT>, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
+    if (hipFuncSetAttribute((const void*)few_rows_kernel<T, DIM, NT, SINKS>, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
       return false;
   }
-  few_rows_kernel<T, DIM, NT><<<dim3((uint32_t)blocks), dim3(64 * kFewWaves), bytes, s>>>(A);
+  few_rows_kernel<T, DIM, NT, SINKS><<<dim3((uint32_t)blocks), dim3(64 * kFewWaves), bytes, s>>>(A);
   return true;
 }
 
-template <typename T, int DIM, bool ONE_PAGE>
+template <typename T, int DIM, bool ONE_PAGE, bool SINKS>
 bool launch_many(const AttnArgs& A, int64_t blocks, hipStream_t s) {
   constexpr int bytes = (int)sizeof(ManyShared<DIM>);
   static_assert(bytes <= 160 * 1024, "LDS of a workgroup");
   if (bytes > 64 * 1024 &&
-      hipFuncSetAttribute((const void*)many_rows_kernel<T, DIM, ONE_PAGE>, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
+      hipFuncSetAttribute((const void*)many_rows_kernel<T, DIM, ONE_PAGE, SINKS>, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
     return false;
-  many_rows_kernel<T, DIM, ONE_PAGE><<<dim3((uint32_t)blocks), dim3(64 * kManyWaves), bytes, s>>>(A);
+  many_rows_kernel<T, DIM, ONE_PAGE, SINKS><<<dim3((uint32_t)blocks), dim3(64 * kManyWaves), bytes, s>>>(A);
   return true;
+}
+
+template <typename T, int DIM, bool SINKS>
+bool launch_rows(const AttnArgs& A, const Plan& p, hipStream_t s) {
+  if constexpr (sizeof(T) == 2)
+    if (p.many)
+      return A.c.page_shift >= 6 ? launch_many<T, DIM, true, SINKS>(A, p.blocks, s) : launch_many<T, DIM, false, SINKS>(A, p.blocks, s);
+  return p.nt == 1 ? launch_few<T, DIM, 1, SINKS>(A, p.blocks, s) : launch_few<T, DIM, 2, SINKS>(A, p.blocks, s);
 }
 
 template <typename T, int DIM>
 void launch_dim(const AttnArgs& A, const Plan& p, hipStream_t s) {
-  bool ok = false;
-  if constexpr (sizeof(T) == 2)
-    if (p.many) ok = A.c.page_shift >= 6 ? launch_many<T, DIM, true>(A, p.blocks, s) : launch_many<T, DIM, false>(A, p.blocks, s);
-  if (!p.many) ok = p.nt == 1 ? launch_few<T, DIM, 1>(A, p.blocks, s) : launch_few<T, DIM, 2>(A, p.blocks, s);
+  const bool ok = A.sinks > 0 ? launch_rows<T, DIM, true>(A, p, s) : launch_rows<T, DIM, false>(A, p, s);
   if (ok && p.splits > 1) {
     const dim3 grid((uint32_t)join_blocks(p, (int64_t)A.s.tokens * A.heads_q));
     if (p.splits <= kFewSplits) join_kernel<T, DIM, 1><<<grid, dim3(256), 0, s>>>(A, p.rows);
@@ -1198,22 +1228,22 @@ void launch_type(const AttnArgs& A, const Plan& p, int64_t dim, hipStream_t s) {
 namespace nvfp4host {
 
 int64_t paged_attention_bytes(int64_t tokens, int64_t heads_q, int64_t heads, int64_t dim, int64_t page, int64_t batch,
-                              int64_t max_q, int64_t width, int64_t window, nvfp4_dtype_t dt) {
-  return (partials(make_plan(heads_q, heads, page, batch, max_q, width, window, dt, dim, true), tokens, heads_q, dim) + 255) / 256 * 256;
+                              int64_t max_q, int64_t width, int64_t window, int64_t sinks, nvfp4_dtype_t dt) {
+  return (partials(make_plan(heads_q, heads, page, batch, max_q, width, window, sinks, dt, dim, true), tokens, heads_q, dim) + 255) / 256 * 256;
 }
 
 int64_t paged_attention_blocks(int64_t tokens, int64_t heads_q, int64_t heads, int64_t dim, int64_t page, int64_t batch,
-                               int64_t max_q, int64_t width, int64_t window, nvfp4_dtype_t dt) {
-  const Plan p = make_plan(heads_q, heads, page, batch, max_q, width, window, dt, dim, true);
+                               int64_t max_q, int64_t width, int64_t window, int64_t sinks, nvfp4_dtype_t dt) {
+  const Plan p = make_plan(heads_q, heads, page, batch, max_q, width, window, sinks, dt, dim, true);
   return std::max(p.blocks, join_blocks(p, tokens * heads_q));
 }
 
 void launch_paged_attention(const nvfp4_kv_cache_t& c, const void* q, int64_t q_token, int64_t q_head, int64_t heads_q,
                             nvfp4_dtype_t dt, int64_t tokens, const int32_t* cu, int64_t batch, int64_t max_q,
-                            const int32_t* table, int64_t width, const int32_t* lens, int64_t window, float scale,
-                            void* ws, int64_t ws_bytes, void* out, hipStream_t s) {
-  Plan p = make_plan(heads_q, c.heads, c.page, batch, max_q, width, window, dt, c.dim, true);
-  if (ws_bytes < partials(p, tokens, heads_q, c.dim)) p = make_plan(heads_q, c.heads, c.page, batch, max_q, width, window, dt, c.dim, false);
+                            const int32_t* table, int64_t width, const int32_t* lens, int64_t window,
+                            int64_t sinks, float scale, void* ws, int64_t ws_bytes, void* out, hipStream_t s) {
+  Plan p = make_plan(heads_q, c.heads, c.page, batch, max_q, width, window, sinks, dt, c.dim, true);
+  if (ws_bytes < partials(p, tokens, heads_q, c.dim)) p = make_plan(heads_q, c.heads, c.page, batch, max_q, width, window, sinks, dt, c.dim, false);
   AttnArgs A;
   A.c = {c.k, c.v, c.k_scales, c.v_scales, (int32_t)c.pages, (int32_t)c.heads, __builtin_ctz((unsigned)c.page)};
   A.s = {table, lens, cu, width, (int32_t)batch, (int32_t)tokens, (int32_t)max_q};
@@ -1227,6 +1257,7 @@ void launch_paged_attention(const nvfp4_kv_cache_t& c, const void* q, int64_t q_
   A.heads_q = (int32_t)heads_q; A.group = (int32_t)(heads_q / c.heads);
   // none where it passes all positions; lengths may pass the table, so its size says nothing
   A.window = window <= 0 || window > INT_MAX ? 0 : (int32_t)window;
+  A.sinks = A.window == 0 || sinks <= 0 ? 0 : (int32_t)std::min<int64_t>(sinks, INT_MAX);
   A.splits = (int32_t)p.splits; A.chunk = (int32_t)p.chunk;
   A.row_tiles = (int32_t)p.row_tiles;
   A.sign = scale < 0.0f ? -1.0f : 1.0f;

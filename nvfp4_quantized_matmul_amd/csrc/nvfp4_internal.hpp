@@ -138,13 +138,13 @@ void launch_kv_append(const nvfp4_kv_cache_t& c, const void* k, int64_t k_token,
 // a split of the token axis wants (0: none), paged_attention_blocks the larger
 // one of its grids.
 int64_t paged_attention_bytes(int64_t tokens, int64_t heads_q, int64_t heads, int64_t dim, int64_t page, int64_t batch,
-                              int64_t max_q, int64_t width, int64_t window, nvfp4_dtype_t dt);
+                              int64_t max_q, int64_t width, int64_t window, int64_t sinks, nvfp4_dtype_t dt);
 int64_t paged_attention_blocks(int64_t tokens, int64_t heads_q, int64_t heads, int64_t dim, int64_t page, int64_t batch,
-                               int64_t max_q, int64_t width, int64_t window, nvfp4_dtype_t dt);
+                               int64_t max_q, int64_t width, int64_t window, int64_t sinks, nvfp4_dtype_t dt);
 void launch_paged_attention(const nvfp4_kv_cache_t& c, const void* q, int64_t q_token, int64_t q_head, int64_t heads_q,
                             nvfp4_dtype_t dt, int64_t tokens, const int32_t* cu, int64_t batch, int64_t max_q,
-                            const int32_t* table, int64_t width, const int32_t* lens, int64_t window, float scale,
-                            void* ws, int64_t ws_bytes, void* out, hipStream_t s);
+                            const int32_t* table, int64_t width, const int32_t* lens, int64_t window,
+                            int64_t sinks, float scale, void* ws, int64_t ws_bytes, void* out, hipStream_t s);
 // The pages' bookkeeping.  kv_reserve_items: page slots that new tokens may
 // reach.
 int64_t kv_reserve_items(int64_t tokens, int64_t batch, int64_t page, bool offsets);

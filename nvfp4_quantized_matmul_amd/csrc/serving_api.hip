@@ -161,9 +161,9 @@ int nvfp4_kv_append(const nvfp4_kv_cache_t* cache, const void* k, int64_t k_toke
   return launched();
 }
 
-int64_t nvfp4_paged_attention_workspace_size(int64_t tokens, int64_t heads_q, int64_t heads, int64_t dim,
-                                             int64_t page, int64_t batch, int64_t max_q,
-                                             int64_t table_width, int64_t window, nvfp4_dtype_t dtype) {
+int64_t nvfp4_paged_attention_sinks_workspace_size(int64_t tokens, int64_t heads_q, int64_t heads, int64_t dim,
+                                                   int64_t page, int64_t batch, int64_t max_q, int64_t table_width,
+                                                   int64_t window, int64_t sinks, nvfp4_dtype_t dtype) {
   int st = check_page(page, dim);
   if (st != NVFP4_OK) return st;
   if (!valid_dtype(dtype)) return NVFP4_ERR_DTYPE;
@@ -171,7 +171,14 @@ int64_t nvfp4_paged_attention_workspace_size(int64_t tokens, int64_t heads_q, in
   st = check_sizes(heads_q, heads, page, tokens, batch, max_q, table_width);
   if (st != NVFP4_OK) return st;
   if (tokens == 0 || batch == 0 || heads_q == 0 || max_q == 0) return 0;
-  return nvfp4host::paged_attention_bytes(tokens, heads_q, heads, dim, page, batch, max_q, table_width, window, dtype);
+  return nvfp4host::paged_attention_bytes(tokens, heads_q, heads, dim, page, batch, max_q, table_width, window, sinks, dtype);
+}
+
+int64_t nvfp4_paged_attention_workspace_size(int64_t tokens, int64_t heads_q, int64_t heads, int64_t dim,
+                                             int64_t page, int64_t batch, int64_t max_q,
+                                             int64_t table_width, int64_t window, nvfp4_dtype_t dtype) {
+  return nvfp4_paged_attention_sinks_workspace_size(tokens, heads_q, heads, dim, page, batch, max_q, table_width, window,
+                                                    0, dtype);
 }
 
 int nvfp4_paged_attention(const nvfp4_kv_cache_t* cache, const void* q, int64_t q_token, int64_t q_head,
@@ -179,6 +186,15 @@ int nvfp4_paged_attention(const nvfp4_kv_cache_t* cache, const void* q, int64_t 
                           int64_t batch, int64_t max_q, const int32_t* table, int64_t table_width,
                           const int32_t* lens, int64_t window, float scale, void* workspace,
                           int64_t workspace_bytes, void* out, hipStream_t stream) {
+  return nvfp4_paged_attention_sinks(cache, q, q_token, q_head, heads_q, dtype, tokens, cu_q, batch, max_q, table,
+                                     table_width, lens, window, 0, scale, workspace, workspace_bytes, out, stream);
+}
+
+int nvfp4_paged_attention_sinks(const nvfp4_kv_cache_t* cache, const void* q, int64_t q_token, int64_t q_head,
+                                int64_t heads_q, nvfp4_dtype_t dtype, int64_t tokens, const int32_t* cu_q,
+                                int64_t batch, int64_t max_q, const int32_t* table, int64_t table_width,
+                                const int32_t* lens, int64_t window, int64_t sinks, float scale, void* workspace,
+                                int64_t workspace_bytes, void* out, hipStream_t stream) {
   int64_t cache_bytes = 0, nq, no;
   int st = check_cache(cache, &cache_bytes);
   if (st != NVFP4_OK) return st;
@@ -206,10 +222,10 @@ int nvfp4_paged_attention(const nvfp4_kv_cache_t* cache, const void* q, int64_t 
                     overlaps(workspace, workspace_bytes, cache->v, cache_bytes)))
     return NVFP4_ERR_SHAPE;
   if (nvfp4host::paged_attention_blocks(tokens, heads_q, cache->heads, cache->dim, cache->page, batch, max_q, table_width, window,
-                                        dtype) > nvfp4host::kMaxGrid256)
+                                        sinks, dtype) > nvfp4host::kMaxGrid256)
     return NVFP4_ERR_GRID;
   nvfp4host::launch_paged_attention(*cache, q, q_token, q_head, heads_q, dtype, tokens, cu_q, batch, max_q, table,
-                                    table_width, lens, window, scale, workspace, workspace_bytes, out, stream);
+                                    table_width, lens, window, sinks, scale, workspace, workspace_bytes, out, stream);
   return launched();
 }
 

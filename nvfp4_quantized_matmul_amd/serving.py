@@ -223,15 +223,16 @@ _ATTENTION_WS_CACHE: dict = {}
 
 def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch.Tensor,
                     cu_q: Optional[torch.Tensor] = None, max_q: Optional[int] = None, window: int = 0,
-                    scale: Optional[float] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                    scale: Optional[float] = None, out: Optional[torch.Tensor] = None, sinks: int = 0) -> torch.Tensor:
     """Causal attention of the new tokens over their sequences' cached ones.
 
     q [tokens, heads, dim] (float32, bfloat16 or float16, any strides of
     tokens and heads), heads a multiple of the cache's; table, lens, cu_q and
     max_q as for kv_append, which has put the new tokens into the cache
-    before.  window > 0: a query sees the last `window` tokens up to its own.
-    scale defaults to dim ** -0.5.  Returns [tokens, heads, dim] in q's dtype,
-    zeros for a query that sees nothing.
+    before.  window > 0: a query sees the last `window` tokens up to its own,
+    and with sinks > 0 the first `sinks` ones of its sequence; pages that none
+    sees are not read.  scale defaults to dim ** -0.5.  Returns [tokens, heads,
+    dim] in q's dtype, zeros for a query that sees nothing.
     """
     code = _dtype_code(q.dtype)
     shape, heads, dim = q.shape, cache._heads, cache._dim
@@ -247,18 +248,18 @@ def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
     if tokens == 0 or heads_q == 0:
         return out
     lib = load_library()
-    key = (tokens, heads_q, heads, dim, cache._page, batch, most, width, window, code)
+    key = (tokens, heads_q, heads, dim, cache._page, batch, most, width, window, sinks, code)
     ws_bytes = _ATTENTION_WS_CACHE.get(key)
     if ws_bytes is None:
-        ws_bytes = int(lib.nvfp4_paged_attention_workspace_size(*key))
+        ws_bytes = int(lib.nvfp4_paged_attention_sinks_workspace_size(*key))
         if ws_bytes < 0:
-            raise NVFP4Error("nvfp4_paged_attention_workspace_size", ws_bytes)
+            raise NVFP4Error("nvfp4_paged_attention_sinks_workspace_size", ws_bytes)
         if len(_ATTENTION_WS_CACHE) < 4096:
             _ATTENTION_WS_CACHE[key] = ws_bytes
     ws = torch.empty(ws_bytes, dtype=_U8, device=cache._device) if ws_bytes else None
-    _check("nvfp4_paged_attention", lib.nvfp4_paged_attention(
+    _check("nvfp4_paged_attention_sinks", lib.nvfp4_paged_attention_sinks(
         cache._ref, q.data_ptr(), qs[0], qs[1], heads_q, code, tokens, cu, batch, most, table.data_ptr(), width,
-        lens.data_ptr(), window, dim ** -0.5 if scale is None else scale, ws.data_ptr() if ws_bytes else None, ws_bytes,
+        lens.data_ptr(), window, sinks, dim ** -0.5 if scale is None else scale, ws.data_ptr() if ws_bytes else None, ws_bytes,
         out.data_ptr(), _stream(cache._device)))
     return out
 
