@@ -478,6 +478,29 @@ int nvfp4_kv_append(const nvfp4_kv_cache_t* cache, const void* k, int64_t k_toke
                     int interleaved, hipStream_t stream);
 
 /*
+ * nvfp4_kv_append_norm -- nvfp4_kv_append whose queries and keys are normed
+ * before their rotation, each head by itself:
+ *
+ *   x -> x / sqrt(mean(x^2) + eps) * weight      over the head's dim channels
+ *
+ *   q_norm, k_norm  float weights, or NULL for no norm on that side: [dim] for
+ *                   all heads with q_norm_head (k_norm_head) 0, [heads_q, dim]
+ *                   ([heads, dim]) with dim
+ *   eps             at least 0
+ *
+ * Sums, norms and rotations are in 64 bits, and each value is rounded to 32
+ * bits behind them and then once to its code, or to q_out.  A row whose mean is
+ * not finite follows the formula: an infinity becomes NaN and finite values 0.
+ */
+int nvfp4_kv_append_norm(const nvfp4_kv_cache_t* cache, const void* k, int64_t k_token, int64_t k_head,
+                         const void* v, int64_t v_token, int64_t v_head, const void* q, int64_t q_token,
+                         int64_t q_head, int64_t heads_q, void* q_out, nvfp4_dtype_t dtype, int64_t tokens,
+                         const int32_t* cu_q, int64_t batch, int64_t max_q, const int32_t* table,
+                         int64_t table_width, const int32_t* lens, const float* inv_freq, int64_t rot,
+                         int interleaved, const float* q_norm, int64_t q_norm_head, const float* k_norm,
+                         int64_t k_norm_head, double eps, hipStream_t stream);
+
+/*
  * nvfp4_paged_attention -- attention of the new tokens over the cached ones.
  *
  *   q    [tokens, heads_q, dim] of dtype, strides q_token, q_head; heads_q is

@@ -83,6 +83,8 @@ def load_library() -> ctypes.CDLL:
         "nvfp4_gather_qmm": [vp, c_int, i64, i64, i64, vp, vp, i64, vp, vp, vp, i64, i64, c_int, vp, vp],
         "nvfp4_kv_append": [vp, vp, i64, i64, vp, i64, i64, vp, i64, i64, i64, vp, c_int, i64, vp, i64, i64, vp, i64,
                             vp, vp, i64, c_int, vp],
+        "nvfp4_kv_append_norm": [vp, vp, i64, i64, vp, i64, i64, vp, i64, i64, i64, vp, c_int, i64, vp, i64, i64, vp,
+                                 i64, vp, vp, i64, c_int, vp, i64, vp, i64, ctypes.c_double, vp],
         "nvfp4_paged_attention_workspace_size": [i64] * 9 + [c_int],
         "nvfp4_paged_attention": [vp, vp, i64, i64, i64, c_int, i64, vp, i64, i64, vp, i64, vp, i64, ctypes.c_float,
                                   vp, i64, vp, vp],

@@ -1,5 +1,5 @@
 // New keys and values into the paged 8-bit cache, with the position rotation
-// of keys and queries.
+// of keys and queries, and before it, if wanted, the norms of their heads.
 //
 // One launch.  A block owns one side (keys or values) of one page and head
 // that a sequence's new tokens reach, so that the page's scale -- the smallest
@@ -16,6 +16,10 @@
 // sines' and cosines' error of up to 4e-13 moves that rounding in 1 of 10^5
 // values at most) and the largest value of a page falls on the right side of a
 // power of two.
+//
+// Norms: x -> x / sqrt(mean(x^2) + eps) * weight over a head's channels, in 64
+// bits too: the sum of squares is exact to 2^-52 and cannot leave the range,
+// and a value is rounded to 32 bits once, behind its rotation.
 //
 // Bound by memory where there is much to do: three ragged prompts of up to 4096
 // tokens, 42 + 2 x 6 heads of 128 (234 MB), take 61 us, 3.8 TB/s (in bf16 with
@@ -46,6 +50,9 @@ struct AppendArgs {
   const float* inv_freq;
   int64_t kv_blocks;
   int32_t heads_q, dim, rot, q_tokens;
+  const float *q_norm, *k_norm;          // weights, or null
+  int64_t q_norm_head, k_norm_head;      // from one head's to the next's
+  double eps;
   int32_t slots;   // page slots of a sequence; 0: as the offsets tell
 };
 
@@ -155,18 +162,90 @@ __device__ __forceinline__ float rounded(double x) {
   return r;
 }
 
-template <int W, bool INTER, typename CS>
-__device__ __forceinline__ void rotate_item(float (&a)[W], float (&b)[W], const CS& cs_of) {
+// `of` makes a double of channel i of a group (0: a, 1: b) from what was loaded.
+template <int W, bool INTER, typename OF, typename CS>
+__device__ __forceinline__ void rotate_item(float (&a)[W], float (&b)[W], const OF& of, const CS& cs_of) {
 #pragma unroll
   for (int i = 0; i < W; ++i) {
     double sn, cs;
     cs_of(i, &sn, &cs);
-    float& xr = INTER ? (2 * i < W ? a[(2 * i) % W] : b[(2 * i) % W]) : a[i];
-    float& yr = INTER ? (2 * i + 1 < W ? a[(2 * i + 1) % W] : b[(2 * i + 1) % W]) : b[i];
-    const double x = xr, y = yr;
+    const int gx = INTER && 2 * i >= W, gy = !INTER || 2 * i + 1 >= W, ix = INTER ? 2 * i % W : i, iy = INTER ? (2 * i + 1) % W : i;
+    float& xr = gx ? b[ix] : a[ix];
+    float& yr = gy ? b[iy] : a[iy];
+    const double x = of(xr, gx, ix), y = of(yr, gy, iy);
     xr = rounded(x * cs - y * sn);
     yr = rounded(y * cs + x * sn);
   }
+}
+
+// Of channels without a norm.
+struct Plain {
+  __device__ __forceinline__ double operator()(float x, int, int) const { return x; }
+};
+
+// A head's row lies with a group of lanes, a power of two that holds its units;
+// a lane has ITEMS items of the row (one of 16 channels; of two channels, of
+// which a row has up to 128, two).
+template <int W>
+struct RowLanes {
+  static constexpr int kItems = W == 1 ? 2 : 1;
+  int units, lanes;   // lanes with items, and all of the group
+  __device__ __forceinline__ explicit RowLanes(int dim) : units(dim / (2 * W * kItems)) {
+    lanes = units <= 4 ? 4 : units <= 8 ? 8 : units <= 16 ? 16 : units <= 32 ? 32 : 64;
+  }
+};
+
+// Sums of a row's lanes; each lane gets it.
+__device__ __forceinline__ double row_sum(double v, int lanes) {
+  for (int off = lanes >> 1; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+  return v;
+}
+
+// The items of a lane: their norm, and each rotated by cs_of(item, i) or not.
+template <int W, int ITEMS>
+struct Normed {
+  float w[ITEMS][2][W];   // the weights of a head's channels, that the lane has
+  __device__ __forceinline__ void weights(const float* norm, bool active, const int (&ca)[ITEMS], const int (&cb)[ITEMS]) {
+#pragma unroll
+    for (int r = 0; r < ITEMS; ++r)
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        w[r][0][i] = norm && active ? norm[ca[r] + i] : 1.0f;
+        w[r][1][i] = norm && active ? norm[cb[r] + i] : 1.0f;
+      }
+  }
+  static __device__ __forceinline__ double squares(const float (&a)[ITEMS][W], const float (&b)[ITEMS][W]) {
+    double s = 0.0;
+#pragma unroll
+    for (int r = 0; r < ITEMS; ++r)
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        s = __builtin_fma((double)a[r][i], (double)a[r][i], s);
+        s = __builtin_fma((double)b[r][i], (double)b[r][i], s);
+      }
+    return s;
+  }
+  template <bool INTER, typename CS>
+  __device__ __forceinline__ void apply(float (&a)[ITEMS][W], float (&b)[ITEMS][W], double factor, const int (&item)[ITEMS],
+                                        int turning, const CS& cs_of) const {
+#pragma unroll
+    for (int r = 0; r < ITEMS; ++r) {
+      const auto of = [&](float x, int g, int i) { return (double)x * (factor * (double)w[r][g][i]); };
+      if (item[r] < turning) {
+        rotate_item<W, INTER>(a[r], b[r], of, [&](int i, double* sn, double* cs) { cs_of(item[r], i, sn, cs); });
+      } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          a[r][i] = rounded(of(a[r][i], 0, i));
+          b[r][i] = rounded(of(b[r][i], 1, i));
+        }
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ double norm_factor(const AppendArgs& A, double squares) {
+  return 1.0 / __builtin_sqrt(squares / A.dim + A.eps);
 }
 
 // The largest of all threads' values; every thread gets it.
@@ -189,6 +268,36 @@ __device__ __forceinline__ uint32_t finite_bits(float x) {
   return u < 0x7f800000u ? u : 0u;
 }
 
+template <int W>
+__device__ __forceinline__ void store_codes(uint8_t* row, int ca, int cb, const float (&a)[W], const float (&b)[W], int up) {
+  if constexpr (W == 1) {
+    row[ca] = (uint8_t)encode(a[0], up);
+    row[cb] = (uint8_t)encode(b[0], up);
+  } else {
+    uint32_t wa[2] = {0, 0}, wb[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      wa[i / 4] |= encode(a[i], up) << (8 * (i % 4));
+      wb[i / 4] |= encode(b[i], up) << (8 * (i % 4));
+    }
+    *(uint2*)(row + ca) = make_uint2(wa[0], wa[1]);
+    *(uint2*)(row + cb) = make_uint2(wb[0], wb[1]);
+  }
+}
+
+// The first n codes of a page of keys, rounded anew.
+__device__ __forceinline__ void recode_keys(uint8_t* codes, int n, int down) {
+  uint4* p = (uint4*)codes;
+  for (int i = threadIdx.x; i < n / 16; i += kThreads) {
+    uint4 w = p[i];
+    w.x = recode(w.x, down);
+    w.y = recode(w.y, down);
+    w.z = recode(w.z, down);
+    w.w = recode(w.w, down);
+    p[i] = w;
+  }
+}
+
 template <typename T, int W, bool INTER>
 __device__ void append_keys(const AppendArgs& A, const T* k, uint8_t* codes, uint8_t* scale, int pos0, int begin,
                             int end, uint32_t* shared) {
@@ -206,7 +315,7 @@ __device__ void append_keys(const AppendArgs& A, const T* k, uint8_t* codes, uin
     load_group<T, W>(row + cb, b);
     if (j < turning) {
       const double p = begin + t;
-      rotate_item<W, INTER>(a, b, [&](int i, double* sn, double* cs) {
+      rotate_item<W, INTER>(a, b, Plain(), [&](int i, double* sn, double* cs) {
         sin_cos(p * (double)A.inv_freq[W * j + i], sn, cs);
       });
     }
@@ -238,24 +347,11 @@ __device__ void append_keys(const AppendArgs& A, const T* k, uint8_t* codes, uin
   const int byte = held > 0 && old > fresh ? old : fresh;
   const int up = 127 - byte;
 
-  auto write = [&](int it, const float (&a)[W], const float (&b)[W]) {
+  const auto write = [&](int it, const float (&a)[W], const float (&b)[W]) {
     const int t = it / per, j = it - t * per;
     int ca, cb;
     item_channels<W, INTER>(j, A.rot, &ca, &cb);
-    uint8_t* row = codes + (int64_t)(held + t) * A.dim;
-    if constexpr (W == 1) {
-      row[ca] = (uint8_t)encode(a[0], up);
-      row[cb] = (uint8_t)encode(b[0], up);
-    } else {
-      uint32_t wa[2] = {0, 0}, wb[2] = {0, 0};
-#pragma unroll
-      for (int i = 0; i < W; ++i) {
-        wa[i / 4] |= encode(a[i], up) << (8 * (i % 4));
-        wb[i / 4] |= encode(b[i], up) << (8 * (i % 4));
-      }
-      *(uint2*)(row + ca) = make_uint2(wa[0], wa[1]);
-      *(uint2*)(row + cb) = make_uint2(wb[0], wb[1]);
-    }
+    store_codes<W>(codes + (int64_t)(held + t) * A.dim, ca, cb, a, b, up);
   };
 #pragma unroll
   for (int r = 0; r < kHeld; ++r) {
@@ -267,18 +363,90 @@ __device__ void append_keys(const AppendArgs& A, const T* k, uint8_t* codes, uin
     value(it, a, b);
     write(it, a, b);
   }
-  if (held > 0 && byte > old) {
-    uint4* p = (uint4*)codes;
-    for (int i = threadIdx.x; i < held * A.dim / 16; i += kThreads) {
-      uint4 w = p[i];
-      w.x = recode(w.x, old - byte);
-      w.y = recode(w.y, old - byte);
-      w.z = recode(w.z, old - byte);
-      w.w = recode(w.w, old - byte);
-      p[i] = w;
-    }
-  }
+  if (held > 0 && byte > old) recode_keys(codes, held * A.dim, old - byte);
   if (threadIdx.x == 0) *scale = (uint8_t)byte;   // every thread read `old` before the barrier in block_max
+}
+
+// append_keys with the norm of each token's head: rows lie with groups of
+// lanes, which sum their squares among themselves.
+template <typename T, int W, bool INTER>
+__device__ void append_normed_keys(const AppendArgs& A, const T* k, const float* norm, uint8_t* codes, uint8_t* scale,
+                                   int pos0, int begin, int end, uint32_t* shared) {
+  constexpr int ITEMS = RowLanes<W>::kItems;
+  const RowLanes<W> row(A.dim);
+  const int tokens = end - begin, turning = A.rot / (2 * W), each = kThreads / row.lanes;   // tokens of a round
+  const int mine = threadIdx.x / row.lanes, lane = threadIdx.x % row.lanes;
+  const bool active = lane < row.units;
+  const int old = *scale;
+  int item[ITEMS], ca[ITEMS], cb[ITEMS];
+#pragma unroll
+  for (int r = 0; r < ITEMS; ++r) {
+    item[r] = lane + r * row.units;
+    item_channels<W, INTER>(item[r], A.rot, &ca[r], &cb[r]);
+  }
+  Normed<W, ITEMS> n;
+  n.weights(norm, active, ca, cb);
+  const auto load = [&](int t, float (&a)[ITEMS][W], float (&b)[ITEMS][W]) {
+#pragma unroll
+    for (int r = 0; r < ITEMS; ++r) {
+      if (active && t < tokens) {
+        load_group<T, W>(k + (int64_t)t * A.k_token + ca[r], a[r]);
+        load_group<T, W>(k + (int64_t)t * A.k_token + cb[r], b[r]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) a[r][i] = b[r][i] = 0.0f;
+      }
+    }
+  };
+  uint32_t top = 0;
+  const auto value = [&](int t, float (&a)[ITEMS][W], float (&b)[ITEMS][W]) {
+    const double squares = row_sum(n.squares(a, b), row.lanes);
+    if (!active || t >= tokens) return;
+    const double p = begin + t;
+    n.template apply<INTER>(a, b, norm ? norm_factor(A, squares) : 1.0, item, turning, [&](int j, int i, double* sn, double* cs) {
+      sin_cos(p * (double)A.inv_freq[W * j + i], sn, cs);
+    });
+#pragma unroll
+    for (int r = 0; r < ITEMS; ++r)
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const uint32_t u = finite_bits(a[r][i]), w = finite_bits(b[r][i]);
+        top = u > top ? u : top;
+        top = w > top ? w : top;
+      }
+  };
+  float xa[kHeld][ITEMS][W], xb[kHeld][ITEMS][W];
+#pragma unroll
+  for (int r = 0; r < kHeld; ++r)
+    if (r * each < tokens) load(r * each + mine, xa[r], xb[r]);
+#pragma unroll
+  for (int r = 0; r < kHeld; ++r)
+    if (r * each < tokens) value(r * each + mine, xa[r], xb[r]);
+  for (int t0 = kHeld * each; t0 < tokens; t0 += each) {
+    float a[ITEMS][W], b[ITEMS][W];
+    load(t0 + mine, a, b);
+    value(t0 + mine, a, b);
+  }
+  const int fresh = scale_byte(block_max(top, shared));
+  const int held = begin - pos0;
+  const int byte = held > 0 && old > fresh ? old : fresh;
+  const int up = 127 - byte;
+  const auto write = [&](int t, const float (&a)[ITEMS][W], const float (&b)[ITEMS][W]) {
+    if (!active || t >= tokens) return;
+#pragma unroll
+    for (int r = 0; r < ITEMS; ++r) store_codes<W>(codes + (int64_t)(held + t) * A.dim, ca[r], cb[r], a[r], b[r], up);
+  };
+#pragma unroll
+  for (int r = 0; r < kHeld; ++r)
+    if (r * each < tokens) write(r * each + mine, xa[r], xb[r]);
+  for (int t0 = kHeld * each; t0 < tokens; t0 += each) {
+    float a[ITEMS][W], b[ITEMS][W];
+    load(t0 + mine, a, b);
+    value(t0 + mine, a, b);
+    write(t0 + mine, a, b);
+  }
+  if (held > 0 && byte > old) recode_keys(codes, held * A.dim, old - byte);
+  if (threadIdx.x == 0) *scale = (uint8_t)byte;
 }
 
 // Values lie with a channel's tokens side by side: a thread takes four tokens
@@ -360,7 +528,63 @@ __device__ void append_values(const AppendArgs& A, const T* v, uint8_t* codes, u
 // In place of a position (of a row past the tokens that the call takes).
 constexpr int kLeftOut = INT_MIN;
 
+// The n tokens from t0 on: a head's row lies with a group of lanes.
 template <typename T, int W, bool INTER>
+__device__ __forceinline__ void norm_queries(const AppendArgs& A, int t0, int n, uint32_t left_out, const double2* turn) {
+  constexpr int ITEMS = RowLanes<W>::kItems;
+  const RowLanes<W> row(A.dim);
+  const int turning = A.rot / (2 * W), half = A.rot / 2, rows = n * A.heads_q, each = kThreads / row.lanes;
+  const int mine = threadIdx.x / row.lanes, lane = threadIdx.x % row.lanes;
+  int item[ITEMS], ca[ITEMS], cb[ITEMS];
+#pragma unroll
+  for (int r = 0; r < ITEMS; ++r) {
+    item[r] = lane + r * row.units;
+    item_channels<W, INTER>(item[r], A.rot, &ca[r], &cb[r]);
+  }
+  Normed<W, ITEMS> norm;
+  if (A.q_norm_head == 0) norm.weights(A.q_norm, lane < row.units, ca, cb);
+  for (int row0 = 0; row0 < rows; row0 += kQueryItems * each) {
+    float a[kQueryItems][ITEMS][W], b[kQueryItems][ITEMS][W];
+#pragma unroll
+    for (int s = 0; s < kQueryItems; ++s) {
+      const int at = row0 + s * each + mine, t = at / A.heads_q, h = at - t * A.heads_q;
+      const bool active = lane < row.units && at < rows && !((left_out >> t) & 1);
+      const T* p = (const T*)A.q + (int64_t)(t0 + t) * A.q_token + (int64_t)h * A.q_head;
+#pragma unroll
+      for (int r = 0; r < ITEMS; ++r) {
+        if (active) {
+          load_group<T, W>(p + ca[r], a[s][r]);
+          load_group<T, W>(p + cb[r], b[s][r]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < W; ++i) a[s][r][i] = b[s][r][i] = 0.0f;
+        }
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < kQueryItems; ++s) {
+      const int at = row0 + s * each + mine, t = at / A.heads_q, h = at - t * A.heads_q;
+      const bool active = lane < row.units && at < rows && !((left_out >> t) & 1);
+      const double squares = row_sum(norm.squares(a[s], b[s]), row.lanes);
+      if (!active) continue;
+      if (A.q_norm_head != 0) norm.weights(A.q_norm + h * A.q_norm_head, true, ca, cb);
+      norm.template apply<INTER>(a[s], b[s], A.q_norm ? norm_factor(A, squares) : 1.0, item, turning,
+                                 [&](int j, int i, double* sn, double* cs) {
+                                   const double2 d = turn[t * half + W * j + i];
+                                   *sn = d.x;
+                                   *cs = d.y;
+                                 });
+      T* out = (T*)A.q_out + ((int64_t)(t0 + t) * A.heads_q + h) * A.dim;
+#pragma unroll
+      for (int r = 0; r < ITEMS; ++r) {
+        store_group<T, W>(out + ca[r], a[s][r]);
+        store_group<T, W>(out + cb[r], b[s][r]);
+      }
+    }
+  }
+}
+
+template <typename T, int W, bool INTER, bool NORM>
 __device__ void rotate_queries(const AppendArgs& A, int64_t block, double2* turn, int* pos) {
   // turn [q_tokens][rot / 2]: (sin, cos); pos [q_tokens]
   const int t0 = (int)block * A.q_tokens;
@@ -398,6 +622,10 @@ __device__ void rotate_queries(const AppendArgs& A, int64_t block, double2* turn
     turn[i] = make_double2(sn, cs);
   }
   __syncthreads();
+  if constexpr (NORM) {
+    norm_queries<T, W, INTER>(A, t0, n, left_out, turn);
+    return;
+  }
   const int per = A.dim / (2 * W), turning = A.rot / (2 * W), row_items = A.heads_q * per;
   // rows [ta, tb), the loads of several items in flight at a time
   const auto rows = [&](int ta, int tb) {
@@ -424,7 +652,7 @@ __device__ void rotate_queries(const AppendArgs& A, int64_t block, double2* turn
           int ca, cb;
           item_channels<W, INTER>(j, A.rot, &ca, &cb);
           if (j < turning)
-            rotate_item<W, INTER>(a[r], b[r], [&](int i, double* sn, double* cs) {
+            rotate_item<W, INTER>(a[r], b[r], Plain(), [&](int i, double* sn, double* cs) {
               const double2 d = turn[t * half + W * j + i];
               *sn = d.x;
               *cs = d.y;
@@ -444,13 +672,13 @@ __device__ void rotate_queries(const AppendArgs& A, int64_t block, double2* turn
   }
 }
 
-template <typename T, int W, bool INTER>
+template <typename T, int W, bool INTER, bool NORM>
 __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs A) {
   __shared__ double2 turn[kTokensWide * 128];
   __shared__ uint32_t shared[kThreads / 64];
   int64_t block = blockIdx.x;
   if (block >= A.kv_blocks) {
-    rotate_queries<T, W, INTER>(A, block - A.kv_blocks, turn, (int*)shared);
+    rotate_queries<T, W, INTER, NORM>(A, block - A.kv_blocks, turn, (int*)shared);
     return;
   }
   const int side = (int)(block & 1);
@@ -485,18 +713,27 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs A) {
   if (begin >= end || id < 0 || id >= A.c.pages) return;
   const int64_t ph = (int64_t)id * A.c.heads + h;
   const int64_t row = s.row0 + (begin - first), page_bytes = (int64_t)A.dim << A.c.page_shift;
-  if (side == 0)
-    append_keys<T, W, INTER>(A, (const T*)A.k + row * A.k_token + h * A.k_head, A.c.k + ph * page_bytes, A.c.ks + ph,
-                             pos0, begin, end, shared);
+  const T* k = (const T*)A.k + row * A.k_token + h * A.k_head;
+  if (side == 0 && NORM)
+    append_normed_keys<T, W, INTER>(A, k, A.k_norm ? A.k_norm + h * A.k_norm_head : nullptr, A.c.k + ph * page_bytes,
+                                    A.c.ks + ph, pos0, begin, end, shared);
+  else if (side == 0)
+    append_keys<T, W, INTER>(A, k, A.c.k + ph * page_bytes, A.c.ks + ph, pos0, begin, end, shared);
   else
     append_values<T, W>(A, (const T*)A.v + row * A.v_token + h * A.v_head, A.c.v + ph * page_bytes, A.c.vs + ph, pos0,
                         begin, end, shared);
 }
 
+template <typename T, int W, bool NORM>
+void launch_order(const AppendArgs& A, bool inter, int64_t blocks, hipStream_t s) {
+  if (inter) append_kernel<T, W, true, NORM><<<dim3((uint32_t)blocks), dim3(kThreads), 0, s>>>(A);
+  else append_kernel<T, W, false, NORM><<<dim3((uint32_t)blocks), dim3(kThreads), 0, s>>>(A);
+}
+
 template <typename T, int W>
 void launch(const AppendArgs& A, bool inter, int64_t blocks, hipStream_t s) {
-  if (inter) append_kernel<T, W, true><<<dim3((uint32_t)blocks), dim3(kThreads), 0, s>>>(A);
-  else append_kernel<T, W, false><<<dim3((uint32_t)blocks), dim3(kThreads), 0, s>>>(A);
+  if (A.q_norm || A.k_norm) launch_order<T, W, true>(A, inter, blocks, s);
+  else launch_order<T, W, false>(A, inter, blocks, s);
 }
 
 // Page slots that get a block a head and side.  A sequence of n new tokens
@@ -538,7 +775,8 @@ void launch_kv_append(const nvfp4_kv_cache_t& c, const void* k, int64_t k_token,
                       int64_t v_token, int64_t v_head, const void* q, int64_t q_token, int64_t q_head,
                       int64_t heads_q, void* q_out, nvfp4_dtype_t dt, int64_t tokens, const int32_t* cu,
                       int64_t batch, int64_t max_q, const int32_t* table, int64_t width, const int32_t* lens,
-                      const float* inv_freq, int64_t rot, bool inter, hipStream_t s) {
+                      const float* inv_freq, int64_t rot, bool inter, const float* q_norm, int64_t q_norm_head,
+                      const float* k_norm, int64_t k_norm_head, double eps, hipStream_t s) {
   AppendArgs A;
   A.c = {c.k, c.v, c.k_scales, c.v_scales, (int32_t)c.pages, (int32_t)c.heads, __builtin_ctz((unsigned)c.page)};
   A.s = {table, lens, cu, width, (int32_t)batch, (int32_t)tokens, (int32_t)max_q};
@@ -546,6 +784,9 @@ void launch_kv_append(const nvfp4_kv_cache_t& c, const void* k, int64_t k_token,
   A.k_token = k_token; A.k_head = k_head; A.v_token = v_token; A.v_head = v_head; A.q_token = q_token; A.q_head = q_head;
   A.q_out = q_out;
   A.inv_freq = inv_freq;
+  A.q_norm = heads_q ? q_norm : nullptr; A.q_norm_head = A.q_norm ? q_norm_head : 0;
+  A.k_norm = k_norm; A.k_norm_head = k_norm ? k_norm_head : 0;
+  A.eps = eps;
   A.heads_q = (int32_t)heads_q; A.dim = (int32_t)c.dim; A.rot = (int32_t)rot;
   const Slots slots = page_slots(c.page, tokens, batch, max_q);
   A.slots = (int32_t)slots.each;

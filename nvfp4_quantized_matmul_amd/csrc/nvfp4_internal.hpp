@@ -133,7 +133,8 @@ void launch_kv_append(const nvfp4_kv_cache_t& c, const void* k, int64_t k_token,
                       int64_t v_token, int64_t v_head, const void* q, int64_t q_token, int64_t q_head,
                       int64_t heads_q, void* q_out, nvfp4_dtype_t dt, int64_t tokens, const int32_t* cu,
                       int64_t batch, int64_t max_q, const int32_t* table, int64_t width, const int32_t* lens,
-                      const float* inv_freq, int64_t rot, bool inter, hipStream_t s);
+                      const float* inv_freq, int64_t rot, bool inter, const float* q_norm, int64_t q_norm_head,
+                      const float* k_norm, int64_t k_norm_head, double eps, hipStream_t s);
 // Attention over the paged cache.  paged_attention_bytes is the workspace that
 // a split of the token axis wants (0: none), paged_attention_blocks the larger
 // one of its grids.

@@ -2,6 +2,7 @@
 // sampling): argument checks and launches.  Every check runs on the host before anything
 // is enqueued; sequence lengths, row offsets and page tables live on the
 // device and are bounded by the kernels.
+#include <cfloat>
 #include <climits>
 #include <cstdint>
 #include <initializer_list>
@@ -124,6 +125,18 @@ int nvfp4_kv_append(const nvfp4_kv_cache_t* cache, const void* k, int64_t k_toke
                     const int32_t* cu_q, int64_t batch, int64_t max_q, const int32_t* table,
                     int64_t table_width, const int32_t* lens, const float* inv_freq, int64_t rot,
                     int interleaved, hipStream_t stream) {
+  return nvfp4_kv_append_norm(cache, k, k_token, k_head, v, v_token, v_head, q, q_token, q_head, heads_q, q_out, dtype,
+                              tokens, cu_q, batch, max_q, table, table_width, lens, inv_freq, rot, interleaved, nullptr,
+                              0, nullptr, 0, 0.0, stream);
+}
+
+int nvfp4_kv_append_norm(const nvfp4_kv_cache_t* cache, const void* k, int64_t k_token, int64_t k_head,
+                         const void* v, int64_t v_token, int64_t v_head, const void* q, int64_t q_token,
+                         int64_t q_head, int64_t heads_q, void* q_out, nvfp4_dtype_t dtype, int64_t tokens,
+                         const int32_t* cu_q, int64_t batch, int64_t max_q, const int32_t* table,
+                         int64_t table_width, const int32_t* lens, const float* inv_freq, int64_t rot,
+                         int interleaved, const float* q_norm, int64_t q_norm_head, const float* k_norm,
+                         int64_t k_norm_head, double eps, hipStream_t stream) {
   int64_t cache_bytes = 0, nk, nv, nq = 0, no = 0;
   int st = check_cache(cache, &cache_bytes);
   if (st != NVFP4_OK) return st;
@@ -135,6 +148,9 @@ int nvfp4_kv_append(const nvfp4_kv_cache_t* cache, const void* k, int64_t k_toke
   if (k_token < 0 || k_head < 0 || v_token < 0 || v_head < 0 || q_token < 0 || q_head < 0) return NVFP4_ERR_SHAPE;
   if (!q) heads_q = 0;
   if (heads_q > kMaxTurnedHeads) return NVFP4_ERR_SHAPE;
+  if (!(eps >= 0.0) || eps > DBL_MAX || (q_norm && !q)) return NVFP4_ERR_SHAPE;
+  if ((q_norm && q_norm_head != 0 && q_norm_head != cache->dim) || (k_norm && k_norm_head != 0 && k_norm_head != cache->dim))
+    return NVFP4_ERR_SHAPE;
   if (!cu_q && tokens != batch) return NVFP4_ERR_SHAPE;
   if (tokens == 0 || batch == 0) return NVFP4_OK;
   if (max_q == 0) return NVFP4_ERR_SHAPE;   // new tokens, and none in any sequence
@@ -142,6 +158,7 @@ int nvfp4_kv_append(const nvfp4_kv_cache_t* cache, const void* k, int64_t k_toke
   if (st != NVFP4_OK) return st;
   if (!k || !v) return NVFP4_ERR_NULLPTR;
   const int64_t size = dtype_size(dtype);
+  if (!aligned(q_norm, 4) || !aligned(k_norm, 4)) return NVFP4_ERR_ALIGN;
   if (!aligned(k, size) || !aligned(v, size) || !aligned(inv_freq, 4) || (q && (!aligned(q, size) || !aligned(q_out, 16))))
     return NVFP4_ERR_ALIGN;
   if (!extent(tokens, cache->heads, cache->dim, k_token, k_head, &nk) || !mul_ok(nk, size, &nk) ||
@@ -153,11 +170,15 @@ int nvfp4_kv_append(const nvfp4_kv_cache_t* cache, const void* k, int64_t k_toke
       return NVFP4_ERR_SHAPE;
     if (overlaps(q_out, no, q, nq) || overlaps(q_out, no, k, nk) || overlaps(q_out, no, v, nv)) return NVFP4_ERR_SHAPE;
     if (overlaps(q_out, no, cache->k, cache_bytes) || overlaps(q_out, no, cache->v, cache_bytes)) return NVFP4_ERR_SHAPE;
+    if ((q_norm && overlaps(q_out, no, q_norm, (q_norm_head ? heads_q : 1) * cache->dim * 4)) ||
+        (k_norm && overlaps(q_out, no, k_norm, (k_norm_head ? cache->heads : 1) * cache->dim * 4)))
+      return NVFP4_ERR_SHAPE;
   }
   if (nvfp4host::kv_append_blocks(cache->page, cache->heads, heads_q, tokens, batch, max_q) > nvfp4host::kMaxGrid256)
     return NVFP4_ERR_GRID;
   nvfp4host::launch_kv_append(*cache, k, k_token, k_head, v, v_token, v_head, q, q_token, q_head, heads_q, q_out, dtype,
-                              tokens, cu_q, batch, max_q, table, table_width, lens, inv_freq, rot, interleaved != 0, stream);
+                              tokens, cu_q, batch, max_q, table, table_width, lens, inv_freq, rot, interleaved != 0, q_norm,
+                              q_norm_head, k_norm, k_norm_head, eps, stream);
   return launched();
 }
 

@@ -21,7 +21,7 @@ from typing import Optional
 
 import torch
 
-from . import NVFP4Error, _check, _dtype_code, _stream, load_library
+from . import NVFP4Error, _check, _dtype_code, _on_device, _stream, load_library
 
 _PAGES = (16, 32, 64, 128, 256)
 _DIMS = (64, 128, 192, 256)
@@ -152,10 +152,21 @@ def _output(out: Optional[torch.Tensor], q: torch.Tensor, shape, cache: KVCache)
     return out
 
 
+def _norm_weights(name: str, w: torch.Tensor, heads: int, cache: KVCache):
+    """The address of a norm's weights, and from one head's to the next's."""
+    if not (w.shape in ((cache._dim,), (heads, cache._dim)) and w.dtype is _F32 and w.get_device() == cache._index
+            and w.is_contiguous()):
+        if w.dtype is not _F32:
+            raise TypeError(f"{name} must be float32, got {w.dtype}")
+        raise ValueError(f"{name} must be [{cache._dim}] or [{heads}, {cache._dim}], contiguous and on the cache's device")
+    return w.data_ptr(), cache._dim if w.dim() == 2 else 0
+
+
 def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch.Tensor,
               q: Optional[torch.Tensor] = None, cu_q: Optional[torch.Tensor] = None, max_q: Optional[int] = None,
               inv_freq: Optional[torch.Tensor] = None, interleaved: bool = False,
-              out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+              out: Optional[torch.Tensor] = None, q_norm: Optional[torch.Tensor] = None,
+              k_norm: Optional[torch.Tensor] = None, eps: float = 1e-6) -> Optional[torch.Tensor]:
     """Writes new keys and values into the cache; returns the rotated queries.
 
     k and v [tokens, kv heads, dim] and q [tokens, heads, dim] (float32,
@@ -172,6 +183,10 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, table: torch.Ten
     (2i, 2i + 1).  A page's scale grows with its largest value, and the codes
     that it held are then rounded anew; the values of a page at one scale are
     off by at most half a step of their codes.
+
+    q_norm, k_norm float32 [dim], or with a row for each head: each head of the
+    queries or keys is normed before its rotation, x / sqrt(mean(x^2) + eps) *
+    weight.
     """
     dtype, shape, index, dim = k.dtype, k.shape, cache._index, cache._dim
     code = _dtype_code(dtype)
@@ -206,14 +221,22 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, table: torch.Ten
             raise ValueError("out without q")
         qp = qo = None
         q_token = q_head = heads_q = 0
+    qn = kn = None
+    qn_head = kn_head = 0
+    if q_norm is not None:
+        if q is None:
+            raise ValueError("q_norm without q")
+        qn, qn_head = _norm_weights("q_norm", q_norm, heads_q, cache)
+    if k_norm is not None:
+        kn, kn_head = _norm_weights("k_norm", k_norm, cache._heads, cache)
     if tokens == 0:
         return out
     if heads_q == 0:
-        qp = qo = None      # a tensor without heads has no address
-    _check("nvfp4_kv_append", load_library().nvfp4_kv_append(
-        cache._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], qp, q_token, q_head, heads_q, qo, code,
-        tokens, cu, batch, most, table.data_ptr(), width, lens.data_ptr(), freq, rot, 1 if interleaved else 0,
-        _stream(cache._device)))
+        qp = qo = qn = None      # a tensor without heads has no address
+    _check("nvfp4_kv_append_norm", _on_device(
+        cache._index, load_library().nvfp4_kv_append_norm, cache._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0],
+        vs[1], qp, q_token, q_head, heads_q, qo, code, tokens, cu, batch, most, table.data_ptr(), width, lens.data_ptr(),
+        freq, rot, 1 if interleaved else 0, qn, qn_head, kn, kn_head, eps, _stream(cache._device)))
     return out
 
 
@@ -257,10 +280,10 @@ def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
         if len(_ATTENTION_WS_CACHE) < 4096:
             _ATTENTION_WS_CACHE[key] = ws_bytes
     ws = torch.empty(ws_bytes, dtype=_U8, device=cache._device) if ws_bytes else None
-    _check("nvfp4_paged_attention_sinks", lib.nvfp4_paged_attention_sinks(
-        cache._ref, q.data_ptr(), qs[0], qs[1], heads_q, code, tokens, cu, batch, most, table.data_ptr(), width,
-        lens.data_ptr(), window, sinks, dim ** -0.5 if scale is None else scale, ws.data_ptr() if ws_bytes else None, ws_bytes,
-        out.data_ptr(), _stream(cache._device)))
+    _check("nvfp4_paged_attention_sinks", _on_device(
+        cache._index, lib.nvfp4_paged_attention_sinks, cache._ref, q.data_ptr(), qs[0], qs[1], heads_q, code, tokens, cu,
+        batch, most, table.data_ptr(), width, lens.data_ptr(), window, sinks, dim ** -0.5 if scale is None else scale,
+        ws.data_ptr() if ws_bytes else None, ws_bytes, out.data_ptr(), _stream(cache._device)))
     return out
 
 
