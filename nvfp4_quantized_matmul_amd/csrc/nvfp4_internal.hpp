@@ -128,7 +128,8 @@ void launch_gather(const void* x, nvfp4_dtype_t dt, int64_t X, int64_t M, int64_
 
 // Appends new tokens to the paged 8-bit cache and rotates queries (heads_q 0:
 // none); kv_append_blocks is its grid.
-int64_t kv_append_blocks(int64_t page, int64_t heads, int64_t heads_q, int64_t tokens, int64_t batch, int64_t max_q);
+int64_t kv_append_blocks(int64_t page, int64_t dim, int64_t heads, int64_t heads_q, int64_t tokens, int64_t batch,
+                         int64_t max_q, bool norm);
 void launch_kv_append(const nvfp4_kv_cache_t& c, const void* k, int64_t k_token, int64_t k_head, const void* v,
                       int64_t v_token, int64_t v_head, const void* q, int64_t q_token, int64_t q_head,
                       int64_t heads_q, void* q_out, nvfp4_dtype_t dt, int64_t tokens, const int32_t* cu,

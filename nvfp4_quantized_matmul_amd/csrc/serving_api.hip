@@ -174,7 +174,7 @@ int nvfp4_kv_append_norm(const nvfp4_kv_cache_t* cache, const void* k, int64_t k
         (k_norm && overlaps(q_out, no, k_norm, (k_norm_head ? cache->heads : 1) * cache->dim * 4)))
       return NVFP4_ERR_SHAPE;
   }
-  if (nvfp4host::kv_append_blocks(cache->page, cache->heads, heads_q, tokens, batch, max_q) > nvfp4host::kMaxGrid256)
+  if (nvfp4host::kv_append_blocks(cache->page, cache->dim, cache->heads, heads_q, tokens, batch, max_q, q_norm || k_norm) > nvfp4host::kMaxGrid256)
     return NVFP4_ERR_GRID;
   nvfp4host::launch_kv_append(*cache, k, k_token, k_head, v, v_token, v_head, q, q_token, q_head, heads_q, q_out, dtype,
                               tokens, cu_q, batch, max_q, table, table_width, lens, inv_freq, rot, interleaved != 0, q_norm,
