@@ -245,7 +245,8 @@ int64_t kv_append_blocks(int64_t page, int64_t dim, int64_t heads, int64_t heads
                          int64_t max_q, bool norm) {
   int64_t n;
   if (__builtin_mul_overflow(page_slots(page, tokens, batch, max_q).all, heads * 2, &n)) return INT64_MAX;
-  if (norm) return n + kv_append_norm_q_blocks(dim, heads_q, tokens, max_q);
+  if (n > kMaxGrid256) return n;
+  if (norm) return kv_append_norm_blocks(n, page, dim, heads_q, tokens, max_q);
   return n + (heads_q > 0 ? (tokens + query_tokens(tokens) - 1) / query_tokens(tokens) : 0);
 }
 

@@ -23,9 +23,9 @@ using namespace nvfp4dev;
 
 // Rounds of a page's keys that stay in registers between the two passes over
 // it; what is over is formed twice.
-constexpr int kHeld = 2;
+constexpr int kHeld = 4;
 // Rounds of queries that are loaded ahead.
-constexpr int kAhead = 3;
+constexpr int kAhead = 2;
 
 // W = 4 or 1 consecutive elements as they are loaded.
 template <typename T, int W>
@@ -75,7 +75,6 @@ struct Row {
   int units, lanes, lane, turning;   // turning: the items of a row that rotate
   int item[kItems], ca[kItems], cb[kItems];
   bool active;
-  float w[kItems][2][W];     // the weights of the lane's channels
 
   static __device__ __host__ __forceinline__ int group(int dim) {
     const int units = dim / (2 * W * kItems);
@@ -93,14 +92,21 @@ struct Row {
       item_channels<W, INTER>(item[r], A.rot, &ca[r], &cb[r]);
     }
   }
-  // Without a branch around single loads, which would wait for one another.
-  __device__ __forceinline__ void weights(const float* norm) {
+};
+
+// The weights of a lane's channels.
+template <int W, int ITEMS>
+struct Weights {
+  float a[ITEMS][W], b[ITEMS][W];
+  // (Loads behind a branch each would wait for one another.)
+  template <typename R>
+  __device__ __forceinline__ void load(const R& row, const float* norm) {
 #pragma unroll
-    for (int r = 0; r < kItems; ++r)
+    for (int r = 0; r < ITEMS; ++r)
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        w[r][0][i] = norm ? norm[ca[r] + i] : 1.0f;
-        w[r][1][i] = norm ? norm[cb[r] + i] : 1.0f;
+        a[r][i] = norm[row.ca[r] + i];
+        b[r][i] = norm[row.cb[r] + i];
       }
   }
 };
@@ -119,94 +125,162 @@ struct RowData {
   }
 };
 
-// The row's values normed (or not) and rotated.  turn: sine and cosine of pair
-// i of item j at [i * stride + j].
-template <typename T, int W, bool INTER>
-__device__ __forceinline__ void norm_row(const AppendArgs& A, const Row<T, W, INTER>& row, const RowData<T, W>& x, bool normed,
-                                         const double2* turn, int stride, float (&a)[Row<T, W, INTER>::kItems][W],
-                                         float (&b)[Row<T, W, INTER>::kItems][W]) {
-  constexpr int ITEMS = Row<T, W, INTER>::kItems;
-  double factor = 1.0;
+// The row's values normed (or not) and rotated; turn(r, i): sine and cosine of
+// pair i of the lane's item r.
+template <typename T, int W, bool INTER, int ITEMS, typename TURN>
+__device__ __forceinline__ void norm_row(const AppendArgs& A, const Row<T, W, INTER>& row, const RowData<T, W>& x,
+                                         const Weights<W, ITEMS>& w, bool normed, const TURN& turn,
+                                         float (&a)[ITEMS][W], float (&b)[ITEMS][W]) {
+  double u[ITEMS][W], v[ITEMS][W];   // the groups' channels
+#pragma unroll
+  for (int r = 0; r < ITEMS; ++r)
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      u[r][i] = (double)x.a[r][i];
+      v[r][i] = (double)x.b[r][i];
+    }
   if (normed) {
     double s = 0.0;
 #pragma unroll
     for (int r = 0; r < ITEMS; ++r)
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        s = __builtin_fma((double)x.a[r][i], (double)x.a[r][i], s);
-        s = __builtin_fma((double)x.b[r][i], (double)x.b[r][i], s);
+        s = __builtin_fma(u[r][i], u[r][i], s);
+        s = __builtin_fma(v[r][i], v[r][i], s);
       }
-    s = row.active ? s : 0.0;
-    s = row_sum(s, row.lanes);
-    factor = inverse_root(__builtin_fma(s, A.inv_dim, A.eps));
+    const double factor = inverse_root(__builtin_fma(row_sum(row.active ? s : 0.0, row.lanes), A.inv_dim, A.eps));
+#pragma unroll
+    for (int r = 0; r < ITEMS; ++r)
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        u[r][i] *= factor * (double)w.a[r][i];
+        v[r][i] *= factor * (double)w.b[r][i];
+      }
   }
-  // channel i of group g
-  const auto at = [&](int r, int g, int i) { return (double)(g ? x.b[r][i] : x.a[r][i]) * (factor * (double)row.w[r][g][i]); };
 #pragma unroll
   for (int r = 0; r < ITEMS; ++r) {
     if (row.item[r] < row.turning) {
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        const int gx = INTER && 2 * i >= W, gy = !INTER || 2 * i + 1 >= W, ix = INTER ? 2 * i % W : i, iy = INTER ? (2 * i + 1) % W : i;
-        const double2 t = turn[i * stride + row.item[r]];
-        const double u = at(r, gx, ix), v = at(r, gy, iy);
-        (gx ? b : a)[r][ix] = rounded(u * t.y - v * t.x);
-        (gy ? b : a)[r][iy] = rounded(v * t.y + u * t.x);
+        double& p = INTER && 2 * i >= W ? v[r][2 * i % W] : u[r][INTER ? 2 * i % W : i];
+        double& q = !INTER || 2 * i + 1 >= W ? v[r][INTER ? (2 * i + 1) % W : i] : u[r][(2 * i + 1) % W];
+        const double2 t = turn(r, i);
+        const double p0 = p;
+        p = p0 * t.y - q * t.x;
+        q = q * t.y + p0 * t.x;
       }
-    } else {
+    }
 #pragma unroll
-      for (int i = 0; i < W; ++i) {
-        a[r][i] = rounded(at(r, 0, i));
-        b[r][i] = rounded(at(r, 1, i));
-      }
+    for (int i = 0; i < W; ++i) {
+      a[r][i] = rounded(u[r][i]);
+      b[r][i] = rounded(v[r][i]);
     }
   }
 }
 
+// The codes of finite values that are at most 448 at the scale.
+template <int W, int ITEMS>
+__device__ __forceinline__ void store_finite_codes(uint8_t* row, int c, const float (&x)[ITEMS][W], int r, int up) {
+  if constexpr (W == 1) {
+    row[c] = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(__builtin_ldexpf(x[r][0], up), 0.0f, 0, false);
+  } else {
+    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(__builtin_ldexpf(x[r][0], up), __builtin_ldexpf(x[r][1], up), 0, false);
+    *(int*)(row + c) = __builtin_amdgcn_cvt_pk_fp8_f32(__builtin_ldexpf(x[r][2], up), __builtin_ldexpf(x[r][3], up), lo, true);
+  }
+}
+
+// Angles: the first round's sines and cosines are formed by all threads into
+// LDS, and those of the step from a round to the next.  Each lane takes its
+// pairs' into registers and turns them on from round to round, which adds 2^-52
+// or so each time.
 template <typename T, int W, bool INTER, int THREADS>
 __device__ void norm_keys(const AppendArgs& A, const T* k, const float* norm, uint8_t* codes, uint8_t* scale, int pos0,
-                          int begin, int end, double2* turn, uint32_t* shared) {
+                          int begin, int end, double2* turn, double2* step, uint32_t* shared) {
   // k: the head's row of the token at position `begin`; codes: the page; pos0: its first position
   constexpr int ITEMS = Row<T, W, INTER>::kItems;
   Row<T, W, INTER> row(A);
   const int tokens = end - begin, each = THREADS / row.lanes, mine = threadIdx.x / row.lanes;   // each: tokens of a round
+  const int half = A.rot / 2;
   const int old = *scale;
   // rows behind the last one are the last one again
   const auto load = [&](int t, RowData<T, W>& x) { x.load(row, k + (int64_t)(t < tokens ? t : tokens - 1) * A.k_token); };
   RowData<T, W> x[kHeld];
 #pragma unroll
-  for (int r = 0; r < kHeld; ++r) load(r * each + mine, x[r]);
-  row.weights(norm);
-  uint32_t top = 0;
-  const auto value = [&](int t0, const RowData<T, W>& x, float (&a)[ITEMS][W], float (&b)[ITEMS][W]) {
-    const int cells = each * row.turning;
-    if (row.turning > 0) {
-      __syncthreads();   // the round before has read
-      for (int at = threadIdx.x; at < W * cells; at += THREADS) {
-        const int i = at / cells, rest = at - i * cells, t = rest / row.turning, j = rest - t * row.turning;
-        double sn, cs;
-        sin_cos((double)(begin + t0 + t) * (double)A.inv_freq[W * j + i], &sn, &cs);
-        turn[at] = make_double2(sn, cs);
-      }
-      __syncthreads();
+  for (int r = 0; r < kHeld; ++r)
+    if (r == 0 || r * each < tokens) load(r * each + mine, x[r]);
+  Weights<W, ITEMS> weights;
+  if (norm) weights.load(row, norm);
+
+  for (int at = threadIdx.x; at < each * half; at += THREADS) {
+    const int t = at / half, f = at - t * half;
+    double sn, cs;
+    sin_cos((double)(begin + t) * (double)A.inv_freq[f], &sn, &cs);
+    turn[at] = make_double2(sn, cs);
+  }
+  if (each < tokens) {
+    for (int f = threadIdx.x; f < half; f += THREADS) {
+      double sn, cs;
+      sin_cos((double)each * (double)A.inv_freq[f], &sn, &cs);
+      step[f] = make_double2(sn, cs);
     }
-    norm_row<T, W, INTER>(A, row, x, norm != nullptr, turn + mine * row.turning, cells, a, b);
+  }
+  __syncthreads();
+  double sn[ITEMS][W], cs[ITEMS][W];
+  const auto first_angles = [&]() {
 #pragma unroll
     for (int r = 0; r < ITEMS; ++r)
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        const uint32_t u = finite_bits(a[r][i]), w = finite_bits(b[r][i]);
-        const uint32_t m = t0 + mine < tokens ? (u > w ? u : w) : 0u;
-        top = m > top ? m : top;
+        const double2 d = row.item[r] < row.turning ? turn[mine * half + W * row.item[r] + i] : make_double2(0.0, 1.0);
+        sn[r][i] = d.x;
+        cs[r][i] = d.y;
       }
   };
-  float a[kHeld][ITEMS][W], b[kHeld][ITEMS][W];
+  const auto turn_on = [&]() {
 #pragma unroll
-  for (int r = 0; r < kHeld; ++r)
-    if (r * each < tokens) value(r * each, x[r], a[r], b[r]);
+    for (int r = 0; r < ITEMS; ++r)
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        if (row.item[r] < row.turning) {
+          const double2 d = step[W * row.item[r] + i];
+          const double s = sn[r][i];
+          sn[r][i] = s * d.y + cs[r][i] * d.x;
+          cs[r][i] = cs[r][i] * d.y - s * d.x;
+        }
+      }
+  };
+  uint32_t top = 0;
+  bool finite = true;      // all values of the lane's rows are
+  const auto value = [&](int t0, const RowData<T, W>& x, float (&a)[ITEMS][W], float (&b)[ITEMS][W]) {
+    norm_row<T, W, INTER>(A, row, x, weights, norm != nullptr, [&](int r, int i) { return make_double2(sn[r][i], cs[r][i]); }, a, b);
+    uint32_t m = 0;
+#pragma unroll
+    for (int r = 0; r < ITEMS; ++r)
+#pragma unroll
+      for (int i = 0; i < W; ++i) m = max(m, max(fbits(a[r][i]) & 0x7fffffffu, fbits(b[r][i]) & 0x7fffffffu));
+    if (m >= 0x7f800000u) {
+      finite = false;
+      m = 0;
+#pragma unroll
+      for (int r = 0; r < ITEMS; ++r)
+#pragma unroll
+        for (int i = 0; i < W; ++i) m = max(m, max(finite_bits(a[r][i]), finite_bits(b[r][i])));
+    }
+    top = t0 + mine < tokens ? max(top, m) : top;
+  };
+  float a[kHeld][ITEMS][W], b[kHeld][ITEMS][W];
+  first_angles();
+#pragma unroll
+  for (int r = 0; r < kHeld; ++r) {
+    if (r * each < tokens) {
+      if (r > 0) turn_on();
+      value(r * each, x[r], a[r], b[r]);
+    }
+  }
   for (int t0 = kHeld * each; t0 < tokens; t0 += each) {
-    load(t0 + mine, x[0]);
     float c[ITEMS][W], d[ITEMS][W];
+    load(t0 + mine, x[0]);
+    turn_on();
     value(t0, x[0], c, d);
   }
   const int fresh = scale_byte(block_max<THREADS>(top, shared));
@@ -215,14 +289,28 @@ __device__ void norm_keys(const AppendArgs& A, const T* k, const float* norm, ui
   const int up = 127 - byte;
   const auto write = [&](int t, const float (&a)[ITEMS][W], const float (&b)[ITEMS][W]) {
     if (!row.active || t >= tokens) return;
+    uint8_t* to = codes + (int64_t)(held + t) * A.dim;
 #pragma unroll
-    for (int r = 0; r < ITEMS; ++r) store_codes<W>(codes + (int64_t)(held + t) * A.dim, row.ca[r], row.cb[r], a[r], b[r], up);
+    for (int r = 0; r < ITEMS; ++r) {
+      if (finite) {
+        store_finite_codes<W>(to, row.ca[r], a, r, up);
+        store_finite_codes<W>(to, row.cb[r], b, r, up);
+      } else {
+        store_codes<W>(to, row.ca[r], row.cb[r], a[r], b[r], up);
+      }
+    }
   };
 #pragma unroll
   for (int r = 0; r < kHeld; ++r)
     if (r * each < tokens) write(r * each + mine, a[r], b[r]);
+  if (kHeld * each < tokens) {
+    first_angles();
+#pragma unroll 1
+    for (int r = 1; r < kHeld; ++r) turn_on();
+  }
   for (int t0 = kHeld * each; t0 < tokens; t0 += each) {
     load(t0 + mine, x[0]);
+    turn_on();
     value(t0, x[0], a[0], b[0]);
     write(t0 + mine, a[0], b[0]);
   }
@@ -247,21 +335,27 @@ __device__ void norm_queries(const AppendArgs& A, int64_t block, int q_heads, in
   const auto load = [&](int h, RowData<T, W>& x) { x.load(row, q + (int64_t)(h < h1 ? h : h1 - 1) * A.q_head); };
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) load(h0 + i * each + mine, x[i]);
-  if (A.q_norm_head == 0) row.weights(A.q_norm);
+  // weights of a head each are loaded a round ahead as well
+  const auto load_weights = [&](int h, Weights<W, ITEMS>& w) { w.load(row, A.q_norm + (h < h1 ? h : h1 - 1) * A.q_norm_head); };
+  Weights<W, ITEMS> weights;
+  if (A.q_norm) load_weights(h0 + mine, weights);
   const int p = there ? row_position(A, (int)t) : kLeftOut;
   const double at = p < 0 ? 0 : p;
-  for (int c = lane; c < A.rot / 2; c += 64) {
-    const int i = c / row.turning, j = c - i * row.turning;
+  for (int f = lane; f < A.rot / 2; f += 64) {
     double sn, cs;
-    sin_cos(at * (double)A.inv_freq[W * j + i], &sn, &cs);
-    turn[c] = make_double2(sn, cs);
+    sin_cos(at * (double)A.inv_freq[f], &sn, &cs);
+    turn[f] = make_double2(sn, cs);
   }
-  __syncthreads();
+  // a wave reads what it wrote itself: in order, if the compiler keeps it
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   if (p == kLeftOut) return;
   for (int h = h0; h < h1; h += each) {
-    if (A.q_norm_head != 0) row.weights(A.q_norm + (h + mine < h1 ? h + mine : h1 - 1) * A.q_norm_head);
+    Weights<W, ITEMS> w = weights;
+    if (A.q_norm_head != 0) load_weights(h + each + mine, weights);
     float a[ITEMS][W], b[ITEMS][W];
-    norm_row<T, W, INTER>(A, row, x[0], A.q_norm != nullptr, turn, row.turning, a, b);
+    norm_row<T, W, INTER>(A, row, x[0], w, A.q_norm != nullptr, [&](int r, int i) { return turn[W * row.item[r] + i]; }, a, b);
 #pragma unroll
     for (int i = 0; i + 1 < kAhead; ++i) x[i] = x[i + 1];
     load(h + kAhead * each + mine, x[kAhead - 1]);
@@ -279,7 +373,7 @@ __device__ void norm_queries(const AppendArgs& A, int64_t block, int q_heads, in
 template <typename T, int W, bool INTER, int THREADS>
 __global__ __launch_bounds__(THREADS) void norm_append_kernel(AppendArgs A, int q_heads, int q_parts) {
   // rounds of keys: up to four pairs a lane; queries: up to 128 a wave
-  __shared__ double2 turn[THREADS * 4];
+  __shared__ double2 turn[THREADS * 4], step[128];
   __shared__ uint32_t shared[THREADS / 64];
   const int64_t block = blockIdx.x;
   if (block >= A.kv_blocks) {
@@ -292,36 +386,45 @@ __global__ __launch_bounds__(THREADS) void norm_append_kernel(AppendArgs A, int 
   if (p.side == 0)
     norm_keys<T, W, INTER, THREADS>(A, (const T*)A.k + p.row * A.k_token + p.head * A.k_head,
                                     A.k_norm ? A.k_norm + p.head * A.k_norm_head : nullptr, A.c.k + p.ph * page_bytes,
-                                    A.c.ks + p.ph, p.pos0, p.begin, p.end, turn, shared);
+                                    A.c.ks + p.ph, p.pos0, p.begin, p.end, turn, step, shared);
   else
     append_values<T, W == 1 ? 1 : 8, THREADS>(A, (const T*)A.v + p.row * A.v_token + p.head * A.v_head, A.c.v + p.ph * page_bytes,
                                  A.c.vs + p.ph, p.pos0, p.begin, p.end, shared);
 }
 
-// Few new tokens a sequence have few rows a page: blocks of one wave then, and
-// a token's queries in parts of one round.
+// Blocks of as many threads as the rows of a page that new tokens can fill keep
+// busy for kHeld rounds.  In blocks of one wave, for few tokens, a token's
+// queries go in parts of one round.
 struct Plan {
-  bool few;
+  int threads;
   int64_t q_heads, q_parts, q_blocks;
 };
 template <int W>
-Plan make_plan(int64_t dim, int64_t heads_q, int64_t tokens, int64_t max_q) {
+Plan make_plan(int64_t page, int64_t dim, int64_t heads_q, int64_t tokens, int64_t max_q) {
   Plan p;
   const int lanes = Row<float, W, false>::group((int)dim);
-  p.few = max_q * lanes <= 64 * kHeld;
-  p.q_heads = p.few && tokens <= 256 ? 64 / lanes : heads_q;
+  const int64_t rows = (max_q < page ? max_q : page) * lanes;
+  p.threads = rows <= 64 * kHeld / 2 ? 64 : rows <= 256 * kHeld ? 256 : 512;
+  p.q_heads = p.threads == 64 && tokens <= 256 ? 64 / lanes : heads_q;
   p.q_parts = heads_q ? (heads_q + p.q_heads - 1) / p.q_heads : 0;
-  const int64_t units = tokens * p.q_parts;
-  p.q_blocks = p.few ? units : (units + 3) / 4;
+  const int64_t waves = p.threads / 64;
+  p.q_blocks = (tokens * p.q_parts + waves - 1) / waves;
   return p;
+}
+
+template <typename T, int W, bool INTER, int THREADS>
+void launch_threads(const AppendArgs& A, const Plan& p, hipStream_t s) {
+  norm_append_kernel<T, W, INTER, THREADS><<<dim3((uint32_t)(A.kv_blocks + p.q_blocks)), dim3(THREADS), 0, s>>>(A, (int)p.q_heads, (int)p.q_parts);
 }
 
 template <typename T, int W, bool INTER>
 void launch(const AppendArgs& A, int64_t max_q, hipStream_t s) {
-  const Plan p = make_plan<W>(A.dim, A.heads_q, A.s.tokens, max_q);
-  const dim3 grid((uint32_t)(A.kv_blocks + p.q_blocks));
-  if (p.few) norm_append_kernel<T, W, INTER, 64><<<grid, dim3(64), 0, s>>>(A, (int)p.q_heads, (int)p.q_parts);
-  else norm_append_kernel<T, W, INTER, 256><<<grid, dim3(256), 0, s>>>(A, (int)p.q_heads, (int)p.q_parts);
+  const Plan p = make_plan<W>(1 << A.c.page_shift, A.dim, A.heads_q, A.s.tokens, max_q);
+  switch (p.threads) {
+    case 64: launch_threads<T, W, INTER, 64>(A, p, s); break;
+    case 256: launch_threads<T, W, INTER, 256>(A, p, s); break;
+    default: launch_threads<T, W, INTER, 512>(A, p, s); break;
+  }
 }
 
 template <typename T>
@@ -334,8 +437,10 @@ void launch_type(const AppendArgs& A, bool vec, bool inter, int64_t max_q, hipSt
 
 namespace nvfp4host {
 
-int64_t kv_append_norm_q_blocks(int64_t dim, int64_t heads_q, int64_t tokens, int64_t max_q) {
-  return std::max(make_plan<4>(dim, heads_q, tokens, max_q).q_blocks, make_plan<1>(dim, heads_q, tokens, max_q).q_blocks);
+int64_t kv_append_norm_blocks(int64_t page_blocks, int64_t page, int64_t dim, int64_t heads_q, int64_t tokens, int64_t max_q) {
+  const Plan a = make_plan<4>(page, dim, heads_q, tokens, max_q), b = make_plan<1>(page, dim, heads_q, tokens, max_q);
+  const auto blocks = [&](const Plan& p) { return (page_blocks + p.q_blocks) * std::max<int64_t>(p.threads / 256, 1); };
+  return std::max(blocks(a), blocks(b));
 }
 
 void launch_kv_append_norm(const nvfp4dev::AppendArgs& A, nvfp4_dtype_t dt, bool vec, bool inter, int64_t max_q, hipStream_t s) {
