@@ -8,7 +8,7 @@
 // 32 bits once, behind its rotation.
 //
 // A head's row lies with a group of lanes that sum their squares among
-// themselves, 8 channels a lane.  Sines and cosines are formed by all lanes
+// themselves, 8 channels of a key or 16 of a query a lane.  Sines and cosines are formed by all lanes
 // together into LDS, in the order in which the rows' lanes read them, which
 // keeps the code short: what a small call waits for is its instructions.
 #include <algorithm>
@@ -27,10 +27,10 @@ constexpr int kHeld = 4;
 // Rounds of queries that are loaded ahead.
 constexpr int kAhead = 2;
 
-// W = 4 or 1 consecutive elements as they are loaded.
+// W = 8, 4 or 1 consecutive elements as they are loaded.
 template <typename T, int W>
 struct Raw {
-  typedef T V __attribute__((ext_vector_type(W)));
+  typedef T V __attribute__((ext_vector_type(W), aligned(W * sizeof(T) < 16 ? W * sizeof(T) : 16)));
   V v;
   __device__ __forceinline__ void load(const T* p) { v = *(const V*)p; }
   __device__ __forceinline__ float operator[](int i) const { return (float)v[i]; }
@@ -53,13 +53,13 @@ __device__ __forceinline__ double moved(double x) {
   return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
-// The sum over groups of 8, 16, 32 or 64 lanes; each of them gets it.  Lanes
+// The sum over groups of 4, 8, 16, 32 or 64 lanes; each of them gets it.  Lanes
 // meet their neighbour, the other pair, the other four and the other eight
 // (mirrored, which is one lane of them) in registers.
 __device__ __forceinline__ double row_sum(double s, int lanes) {
   s += moved<0xb1>(s);      // lanes 1 0 3 2 of four
   s += moved<0x4e>(s);      // 2 3 0 1
-  s += moved<0x141>(s);     // 7 .. 0 of eight
+  if (lanes >= 8) s += moved<0x141>(s);    // 7 .. 0 of eight
   if (lanes >= 16) s += moved<0x140>(s);   // 15 .. 0 of sixteen
   if (lanes >= 32) s += __shfl_xor(s, 16, 64);
   if (lanes >= 64) s += __shfl_xor(s, 32, 64);
@@ -78,7 +78,7 @@ struct Row {
 
   static __device__ __host__ __forceinline__ int group(int dim) {
     const int units = dim / (2 * W * kItems);
-    return units <= 8 ? 8 : units <= 16 ? 16 : units <= 32 ? 32 : 64;
+    return units <= 4 ? 4 : units <= 8 ? 8 : units <= 16 ? 16 : units <= 32 ? 32 : 64;
   }
   __device__ __forceinline__ explicit Row(const AppendArgs& A) {
     units = A.dim / (2 * W * kItems);
@@ -377,7 +377,7 @@ __global__ __launch_bounds__(THREADS) void norm_append_kernel(AppendArgs A, int 
   __shared__ uint32_t shared[THREADS / 64];
   const int64_t block = blockIdx.x;
   if (block >= A.kv_blocks) {
-    norm_queries<T, W, INTER, THREADS>(A, block - A.kv_blocks, q_heads, q_parts, turn);
+    norm_queries<T, W == 1 ? 1 : 8, INTER, THREADS>(A, block - A.kv_blocks, q_heads, q_parts, turn);
     return;
   }
   PagePart p;
@@ -405,7 +405,7 @@ Plan make_plan(int64_t page, int64_t dim, int64_t heads_q, int64_t tokens, int64
   const int lanes = Row<float, W, false>::group((int)dim);
   const int64_t rows = (max_q < page ? max_q : page) * lanes;
   p.threads = rows <= 64 * kHeld / 2 ? 64 : rows <= 256 * kHeld ? 256 : 512;
-  p.q_heads = p.threads == 64 && tokens <= 256 ? 64 / lanes : heads_q;
+  p.q_heads = p.threads == 64 && tokens <= 256 ? 64 / Row<float, W == 1 ? 1 : 8, false>::group((int)dim) : heads_q;
   p.q_parts = heads_q ? (heads_q + p.q_heads - 1) / p.q_heads : 0;
   const int64_t waves = p.threads / 64;
   p.q_blocks = (tokens * p.q_parts + waves - 1) / waves;
