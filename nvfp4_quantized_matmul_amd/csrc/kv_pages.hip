@@ -19,7 +19,7 @@ namespace {
 using namespace nvfp4dev;
 
 constexpr int kThreads = 256;
-// Table cells of a block.
+// Cells of the table that a block takes.
 constexpr int kCells = 4 * kThreads;
 // Threads of the block that plans, and pages that a thread looks at in a round.
 constexpr int kPlan = 1024, kScan = 16;
@@ -86,17 +86,25 @@ struct FreeArgs {
 };
 
 __global__ __launch_bounds__(kThreads) void free_kernel(FreeArgs A) {
+  // a thread's cells at once: their loads wait together
+  constexpr int N = kCells / kThreads;
+  uint32_t c[N];
+  int32_t id[N], len[N], i[N];
 #pragma unroll
-  for (int r = 0; r < kCells / kThreads; ++r) {
-    const int64_t c = (int64_t)blockIdx.x * kCells + r * kThreads + threadIdx.x;
-    if (c >= A.cells) return;
-    const int32_t b = (int32_t)c / A.width, i = (int32_t)c - b * A.width;
-    const int64_t len = A.lens[b], begin = (int64_t)i << A.page_shift, end = begin + (1 << A.page_shift);
-    if (begin < len && (A.keep <= 0 || end > len - A.keep || begin < A.sinks)) continue;
-    const int32_t id = A.table[c];
-    if (is_page(id, A.pages)) {
-      A.table[c] = -1;
-      atomicSub(&A.refs[id], 1);
+  for (int r = 0; r < N; ++r) {
+    c[r] = blockIdx.x * (uint32_t)kCells + r * kThreads + threadIdx.x;
+    const uint32_t at = c[r] < (uint32_t)A.cells ? c[r] : 0, b = at / (uint32_t)A.width;
+    i[r] = (int32_t)(at - b * (uint32_t)A.width);
+    len[r] = A.lens[b];
+    id[r] = A.table[at];
+  }
+#pragma unroll
+  for (int r = 0; r < N; ++r) {
+    const int64_t begin = (int64_t)i[r] << A.page_shift, end = begin + (1 << A.page_shift);
+    const bool needed = begin < len[r] && (A.keep <= 0 || end > len[r] - A.keep || begin < A.sinks);
+    if (c[r] < (uint32_t)A.cells && !needed && is_page(id[r], A.pages)) {
+      A.table[c[r]] = -1;
+      atomicSub(&A.refs[id[r]], 1);
     }
   }
 }
@@ -105,31 +113,36 @@ struct ForkArgs {
   const int32_t *table, *lens, *parent;
   int32_t *refs, *table_out, *lens_out;
   int32_t batch, rows, width, pages;
-  int64_t cells;   // of the larger table, and at least its rows
+  uint32_t cells;   // of the larger table, and at least its rows
 };
 
 __global__ __launch_bounds__(kThreads) void fork_kernel(ForkArgs A) {
+  constexpr int N = kCells / kThreads;
+  const uint32_t c0 = blockIdx.x * (uint32_t)kCells + threadIdx.x, width = A.width > 0 ? A.width : 1;
+  uint32_t b[N], i[N];
+  int32_t from[N], to[N], parent[N];
 #pragma unroll
-  for (int r = 0; r < kCells / kThreads; ++r) {
-    const int64_t c = (int64_t)blockIdx.x * kCells + r * kThreads + threadIdx.x;
-    if (c >= A.cells) return;
-    if (c < A.rows) {
-      const int32_t p = A.parent[c];
-      A.lens_out[c] = is_page(p, A.batch) ? A.lens[p] : 0;
-    }
-    if (A.width == 0) continue;
-    const int32_t b = (int32_t)c / A.width, i = (int32_t)c - b * A.width;
-    int32_t from = -1, to = -1;
-    if (b < A.batch) from = A.table[c];
-    if (b < A.rows) {
-      const int32_t p = A.parent[b];
-      if (is_page(p, A.batch)) to = A.table[(int64_t)p * A.width + i];
-      A.table_out[c] = to;
+  for (int r = 0; r < N; ++r) {
+    const uint32_t c = c0 + r * kThreads;
+    b[r] = c / width;
+    i[r] = c - b[r] * width;
+    parent[r] = b[r] < (uint32_t)A.rows && c < A.cells ? A.parent[b[r]] : -1;
+    from[r] = A.width > 0 && b[r] < (uint32_t)A.batch ? A.table[c] : -1;
+  }
+#pragma unroll
+  for (int r = 0; r < N; ++r) to[r] = A.width > 0 && is_page(parent[r], A.batch) ? A.table[(int64_t)parent[r] * A.width + i[r]] : -1;
+#pragma unroll
+  for (int r = 0; r < N; ++r) {
+    const uint32_t c = c0 + r * kThreads;
+    if (b[r] < (uint32_t)A.rows && c < A.cells) {
+      if (A.width > 0) A.table_out[c] = to[r];
+      if (i[r] == 0) A.lens_out[b[r]] = is_page(parent[r], A.batch) ? A.lens[parent[r]] : 0;
     }
     // what a row keeps counts as before
-    if (from == to) continue;
-    if (is_page(to, A.pages)) atomicAdd(&A.refs[to], 1);
-    if (is_page(from, A.pages)) atomicSub(&A.refs[from], 1);
+    if (from[r] != to[r]) {
+      if (is_page(to[r], A.pages)) atomicAdd(&A.refs[to[r]], 1);
+      if (is_page(from[r], A.pages)) atomicSub(&A.refs[from[r]], 1);
+    }
   }
 }
 
@@ -332,35 +345,28 @@ struct CopyArgs {
   const int32_t* copies;
   int64_t page_bytes;       // of a side
   int32_t heads, layers, pieces;
-  int32_t table_blocks;     // blocks before the copying ones that rewrite the table
-  int32_t* table;
+  int32_t* table;           // to be rewritten by `where`, by the last row of blocks
   const int32_t* where;
   int32_t cells, pages;
   uint8_t *k[kLayers], *v[kLayers], *ks[kLayers], *vs[kLayers];
 };
 
+// A row of blocks for each cache and side, and one for the table.
 __global__ __launch_bounds__(kThreads) void copy_kernel(CopyArgs A) {
-  if ((int)blockIdx.x < A.table_blocks) {
-#pragma unroll
-    for (int r = 0; r < kCells / kThreads; ++r) {
-      const int64_t c = (int64_t)blockIdx.x * kCells + r * kThreads + threadIdx.x;
-      if (c >= A.cells) return;
+  const int layer = blockIdx.y >> 1, side = blockIdx.y & 1;
+  if (layer == A.layers) {
+    for (uint32_t c = blockIdx.x * kThreads + threadIdx.x; c < (uint32_t)A.cells; c += gridDim.x * kThreads) {
       const int32_t id = A.table[c];
       if (is_page(id, A.pages)) A.table[c] = A.where[id];
     }
     return;
   }
-  const int64_t all = (int64_t)A.copies[0] * A.layers * 2 * A.pieces, step = gridDim.x - A.table_blocks;
-  for (int64_t at = blockIdx.x - A.table_blocks; at < all; at += step) {
-    int64_t rest = at;
-    const int piece = (int)(rest % A.pieces);
-    rest /= A.pieces;
-    const int side = (int)(rest & 1);
-    rest >>= 1;
-    const int layer = (int)(rest % A.layers);
-    const int64_t pair = rest / A.layers;
+  // pieces of all pages of a pool of 2^31 pages would pass 32 bits, those of one in memory do not
+  const uint32_t all = (uint32_t)A.copies[0] * (uint32_t)A.pieces;
+  uint8_t* const base = side ? A.v[layer] : A.k[layer];
+  for (uint32_t at = blockIdx.x; at < all; at += gridDim.x) {
+    const uint32_t pair = at / (uint32_t)A.pieces, piece = at - pair * (uint32_t)A.pieces;
     const int64_t from = A.copies[4 + 2 * pair], to = A.copies[5 + 2 * pair];
-    uint8_t* base = side ? A.v[layer] : A.k[layer];
     const uint4* src = (const uint4*)(base + from * A.page_bytes);
     uint4* dst = (uint4*)(base + to * A.page_bytes);
     const int64_t vecs = A.page_bytes / 16, first = (int64_t)piece * (kPiece / 16) + threadIdx.x;
@@ -393,15 +399,15 @@ void launch_copies(const nvfp4_kv_cache_t* caches, int64_t count, const int32_t*
   A.cells = (int32_t)cells;
   for (int64_t at = 0; at < count; at += kLayers) {
     A.layers = (int32_t)std::min<int64_t>(kLayers, count - at);
-    A.table_blocks = at == 0 && table ? (int32_t)blocks_of(cells) : 0;
+    const bool rewrite = at == 0 && cells > 0;
     for (int i = 0; i < kLayers; ++i) {
       const nvfp4_kv_cache_t& c = caches[at + (i < A.layers ? i : 0)];
       A.k[i] = c.k; A.v[i] = c.v; A.ks[i] = c.k_scales; A.vs[i] = c.v_scales;
     }
-    int64_t copying = kCopyBlocks;
-    if (most < kCopyBlocks) copying = std::min(copying, most * A.layers * 2 * std::min<int64_t>(A.pieces, kCopyBlocks));
-    const int64_t blocks = A.table_blocks + copying;
-    if (blocks > 0) copy_kernel<<<dim3((uint32_t)blocks), dim3(kThreads), 0, s>>>(A);
+    const int64_t row = std::max<int64_t>(kCopyBlocks / (2 * A.layers), 1);
+    int64_t x = most < row ? std::min(row, most * std::min<int64_t>(A.pieces, row)) : row;
+    if (rewrite) x = std::max(x, std::min(blocks_of(cells), row));
+    if (x > 0) copy_kernel<<<dim3((uint32_t)x, (uint32_t)(2 * A.layers + (rewrite ? 1 : 0))), dim3(kThreads), 0, s>>>(A);
   }
 }
 
@@ -430,7 +436,7 @@ void launch_kv_fork(const int32_t* table, int64_t batch, int64_t width, const in
                     int64_t rows, int32_t* refs, int64_t pages, int32_t* table_out, int32_t* lens_out, hipStream_t s) {
   const int64_t cells = std::max(std::max(batch, rows) * width, rows);
   const ForkArgs A = {table, lens, parent, refs, table_out, lens_out, (int32_t)batch, (int32_t)rows, (int32_t)width,
-                      (int32_t)pages, cells};
+                      (int32_t)pages, (uint32_t)cells};
   fork_kernel<<<dim3((uint32_t)blocks_of(cells)), dim3(kThreads), 0, s>>>(A);
 }
 

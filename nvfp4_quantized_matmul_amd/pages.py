@@ -27,49 +27,49 @@ from . import NVFP4Error, _check, _on_device, _stream, load_library
 from .serving import _I32, _PAGES, _U8, KVCache, _CacheStruct
 
 
-def _ints(index: int, **tensors: torch.Tensor) -> None:
-    """Refuses what is not a contiguous int32 tensor on device `index`."""
+# As for the operators that a step calls beside these, a call's checks are one
+# expression, and what is wrong is worked out only once it fails.
+
+def _refuse(index: int, **tensors: torch.Tensor) -> None:
+    """Raises for a tensor that is not contiguous int32 on device `index`, or else for a shape."""
     for name, t in tensors.items():
         if t.dtype is not _I32:
             raise TypeError(f"{name} must be int32, got {t.dtype}")
+        if t.get_device() < 0:
+            raise ValueError("all tensors must be on the GPU")
         if t.get_device() != index:
             raise ValueError(f"{name} must be on the same GPU as the others")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
+    raise ValueError("table must be [batch, width], lens [batch] and refs [pages]: got "
+                     + ", ".join(f"{name} {tuple(t.shape)}" for name, t in tensors.items()))
 
 
-def _table(table: torch.Tensor, refs: torch.Tensor, index: Optional[int] = None) -> Tuple[int, int, int, int]:
-    """(device index, batch, width, pages) of a table and its counts, checked."""
-    if index is None:
-        index = table.get_device()
-        if index < 0:
-            raise ValueError("all tensors must be on the GPU")
-    _ints(index, table=table, refs=refs)
-    if table.dim() != 2 or refs.dim() != 1:
-        raise ValueError("table must be [batch, width] and refs [pages]")
-    return index, table.shape[0], table.shape[1], refs.shape[0]
+def _table(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor) -> Tuple[int, int, int, int]:
+    """(device index, batch, width, pages) of a table, lengths and counts, checked."""
+    index, shape, pages = table.get_device(), table.shape, refs.shape
+    if not (index >= 0 and len(shape) == 2 and len(pages) == 1 and lens.shape == (shape[0],) and table.dtype is _I32
+            and lens.dtype is _I32 and refs.dtype is _I32 and lens.get_device() == index == refs.get_device()
+            and table.is_contiguous() and lens.is_contiguous() and refs.is_contiguous()):
+        _refuse(index, table=table, lens=lens, refs=refs)
+    return index, shape[0], shape[1], pages[0]
 
 
-def _per_sequence(name: str, t: torch.Tensor, n: int, index: int) -> None:
-    _ints(index, **{name: t})
-    if t.shape != (n,):
-        raise ValueError(f"{name} must be [{n}], got {tuple(t.shape)}")
-
-
-def _layers(caches: Union[KVCache, Sequence[KVCache]], refs: torch.Tensor):
+def _layers(caches: Union[KVCache, Sequence[KVCache]], index: int, pages: int):
     """(first cache, their number, nvfp4_kv_cache_t array), checked."""
     if isinstance(caches, KVCache):
         caches = (caches,)
-    if len(caches) == 0:
+    count = len(caches)
+    if count == 0:
         raise ValueError("there is no cache")
     first = caches[0]
-    shape, index = first._k.shape, first._index
+    shape = first._k.shape
     for c in caches:
-        if c._k.shape != shape or c._index != index:
-            raise ValueError("the caches must be of one shape and on one GPU")
-    if refs.shape != (first._pages,):
-        raise ValueError(f"refs {tuple(refs.shape)} must have one count for each of the {first._pages} pages")
-    return first, len(caches), (_CacheStruct * len(caches))(*[c._struct for c in caches])
+        if c._index != index or c._k.shape != shape:
+            raise ValueError("the caches must be of one shape and on the table's GPU")
+    if pages != first._pages:
+        raise ValueError(f"refs must have one count for each of the {first._pages} pages, got {pages}")
+    return first, count, (_CacheStruct * count)(*[c._struct for c in caches])
 
 
 def kv_free(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page: int, keep: int = 0,
@@ -84,8 +84,7 @@ def kv_free(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page: i
     sequence that has ended has length 0.  A window of w tokens with n new ones
     a step needs keep = w + n - 1.
     """
-    index, batch, width, pages = _table(table, refs)
-    _per_sequence("lens", lens, batch, index)
+    index, batch, width, pages = _table(table, lens, refs)
     if page not in _PAGES:
         raise ValueError(f"page must be one of {_PAGES}, got {page}")
     _check("nvfp4_kv_free", _on_device(
@@ -122,17 +121,17 @@ def kv_reserve(caches: Union[KVCache, Sequence[KVCache]], table: torch.Tensor, l
     are free keeps its entries as they are; no token may be appended to it
     before a later call has served it.
     """
-    index, batch, width, _ = _table(table, refs)
-    first, count, structs = _layers(caches, refs)
-    if first._index != index:
-        raise ValueError("table must be on the caches' device")
-    _per_sequence("lens", lens, batch, index)
+    index, batch, width, pages = _table(table, lens, refs)
+    first, count, structs = _layers(caches, index, pages)
     if cu_q is None:
         if tokens is not None and tokens != batch:
             raise ValueError(f"without cu_q every sequence has one new token: {tokens} tokens, {batch} sequences")
         tokens = batch
     else:
-        _per_sequence("cu_q", cu_q, batch + 1, index)
+        if not (cu_q.shape == (batch + 1,) and cu_q.dtype is _I32 and cu_q.get_device() == index and cu_q.is_contiguous()):
+            if cu_q.shape != (batch + 1,):
+                raise ValueError(f"cu_q must be [{batch + 1}], got {tuple(cu_q.shape)}")
+            _refuse(index, cu_q=cu_q)
         if tokens is None:
             raise ValueError("with cu_q, tokens says how many rows there are")
     ws_bytes = _workspace("nvfp4_kv_reserve_workspace_size", tokens, batch, first._page)
@@ -155,18 +154,18 @@ def kv_fork(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, parent:
     entries of the new table and those of the present one, which is not used
     any more.  out: the new table, int32 [rows, width], if given.
     """
-    index, batch, width, pages = _table(table, refs)
-    _per_sequence("lens", lens, batch, index)
-    _ints(index, parent=parent)
-    if parent.dim() != 1:
-        raise ValueError("parent must be 1-D")
+    index, batch, width, pages = _table(table, lens, refs)
+    if not (parent.dim() == 1 and parent.dtype is _I32 and parent.get_device() == index and parent.is_contiguous()):
+        if parent.dim() != 1:
+            raise ValueError("parent must be 1-D")
+        _refuse(index, parent=parent)
     rows = parent.shape[0]
     if out is None:
         out = torch.empty(rows, width, dtype=_I32, device=table.device)
-    else:
-        _ints(index, out=out)
+    elif not (out.shape == (rows, width) and out.dtype is _I32 and out.get_device() == index and out.is_contiguous()):
         if out.shape != (rows, width):
             raise ValueError(f"out must be {(rows, width)}, got {tuple(out.shape)}")
+        _refuse(index, out=out)
     lens_out = torch.empty(rows, dtype=_I32, device=table.device)
     _check("nvfp4_kv_fork", _on_device(
         index, load_library().nvfp4_kv_fork, table.data_ptr(), batch, width, lens.data_ptr(), parent.data_ptr(), rows,
@@ -183,10 +182,12 @@ def kv_compact(caches: Union[KVCache, Sequence[KVCache]], table: torch.Tensor, r
     the new place of each page that was in use, -1 for the others.  The k-th
     page in use at or behind `used` goes to the k-th free one before it.
     """
-    index, batch, width, pages = _table(table, refs)
-    first, count, structs = _layers(caches, refs)
-    if first._index != index:
-        raise ValueError("table must be on the caches' device")
+    index, shape = table.get_device(), table.shape
+    if not (index >= 0 and len(shape) == 2 and refs.dim() == 1 and table.dtype is _I32 and refs.dtype is _I32
+            and refs.get_device() == index and table.is_contiguous() and refs.is_contiguous()):
+        _refuse(index, table=table, refs=refs)
+    (batch, width), pages = shape, refs.shape[0]
+    _, count, structs = _layers(caches, index, pages)
     ws_bytes = _workspace("nvfp4_kv_compact_workspace_size", pages)
     ws = torch.empty(ws_bytes, dtype=_U8, device=table.device)
     used = torch.empty(1, dtype=_I32, device=table.device)
