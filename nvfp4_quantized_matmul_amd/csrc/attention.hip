@@ -271,11 +271,10 @@ constexpr int few_lds_bytes() {
 // spill 25 at two blocks (32 sequences of up to 8k tokens, 16 heads, take 38 us,
 // 41 with one block and no spill; 4 of up to 87k 199 us, and 183), 32 rows of
 // 256 spill 82, and 107 in float32, at one.
-template <int DIM, int NT, int PARTS>
-constexpr int few_blocks_per_cu() { return NT * DIM / 4 + 16 * NT + DIM / 2 + 24 * PARTS * NT + 64 <= 256 ? 2 : 1; }
+constexpr int few_blocks_per_cu(int dim, int nt, int parts) { return nt * dim / 4 + 16 * nt + dim / 2 + 24 * parts * nt + 64 <= 256 ? 2 : 1; }
 
 template <typename T, int DIM, int NT, bool SINKS>
-__global__ __launch_bounds__(64 * kFewWaves, (few_blocks_per_cu<DIM, NT, Mma<T>::kParts>())) void few_rows_kernel(AttnArgs A) {
+__global__ __launch_bounds__(64 * kFewWaves, few_blocks_per_cu(DIM, NT, Mma<T>::kParts)) void few_rows_kernel(AttnArgs A) {
   typedef Mma<T> M;
   typedef typename M::V8 V8;
   constexpr int PARTS = M::kParts, U = DIM / 64, CB = DIM / 16, ROWS = 16 * NT;
@@ -1150,9 +1149,16 @@ Plan make_plan(int64_t heads_q, int64_t heads, int64_t page, int64_t batch, int6
   p.chunk = (tiles > 0 ? tiles : 1) * 64;
   if (split) {
     // few rows: three rounds of blocks on the chip, and four tiles a wave at
-    // least; many rows: one round, and eight tiles a block
-    const int64_t unit = p.many ? 1 : kFewWaves, least = p.many ? 8 : 4 * kFewWaves, full = p.many ? (dim <= 64 ? 768 : 512) : 3 * 512;
-    int64_t want = p.many ? full / base : (full + base - 1) / base;
+    // least; many rows: one round, and eight tiles a block.  With sinks, which
+    // go with a window that is short beside the sequences, spans are alike: few
+    // rows then take the one round that comes nearest, and two tiles a wave (32
+    // heads of 128 over 8, 4096 + 4 tokens: 64 sequences 98 us, 111 with three
+    // rounds; 16 28.7 and 36; one 11.7 and 13.8; 16 of 6 tokens 36 and 54)
+    const bool alike = sinks > 0 && window > 0;
+    const int64_t unit = p.many ? 1 : kFewWaves, least = p.many ? 8 : (alike ? 2 : 4) * kFewWaves;
+    const int64_t round = 256 * few_blocks_per_cu((int)dim, p.nt, dt == NVFP4_F32 ? 3 : 1);
+    const int64_t full = p.many ? (dim <= 64 ? 768 : 512) : alike ? round + base / 2 : 3 * 512 + base - 1;
+    int64_t want = full / base;
     const int64_t most = (tiles + least - 1) / least;
     if (want > most) want = most;
     if (want > 1) {
