@@ -694,7 +694,6 @@ struct ManyShared {
   ManyTile<DIM> tile[2];
   GroupInfo info[2][4];
   uint32_t there[2];   // bit g: group g's page is there
-  uint32_t far[2];     // some group's rest is not 1
   int32_t nan[2];      // the first token of the last partial tile here that had a NaN code among its values,
   __align__(8) uint16_t nan_tokens[2][DIM][4];   // and which ones: a bit per token
 };
@@ -855,11 +854,8 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1
     if (wave == 0) {
       const ValueScale vs = value_scale<T>(vbyte);
       if (tid < 4) S.info[at][tid] = {__builtin_ldexpf(A.scale_log2, kbyte - 127), vs.e, vs.rest, vs.back};
-      const uint64_t there = __ballot(id[VALUES] >= 0), far = __ballot(vs.rest != 1.0f);
-      if (tid == 0) {
-        S.there[at] = (uint32_t)there & 0xfu;
-        S.far[at] = (uint32_t)far & 0xfu;
-      }
+      const uint64_t there = __ballot(id[VALUES] >= 0);
+      if (tid == 0) S.there[at] = (uint32_t)there & 0xfu;
     }
   };
 
@@ -970,29 +966,20 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1
         for (int c = 0; c < CB; ++c) o[c] *= alpha;
       }
       const float base = m == -__builtin_inff() ? 0.0f : m;
+      // rest is 1 but for values of very different scales
       V8 pw[4];
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const float back = S.info[at][g].back, less = add[g] - base;
+        const float back = S.info[at][g].back, rest = S.info[at][g].rest, less = add[g] - base;
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float w = pow2(__builtin_fmaf(sc[g / 2][8 * (g % 2) + j], mul[g], less));
-          sc[g / 2][8 * (g % 2) + j] = w;
           sum += w;
+          pw[g][j] = (E)(w * rest);
         }
         l = __builtin_fmaf(sum, back, l);
       }
-      if (S.far[at]) {
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) sc[g / 2][8 * (g % 2) + j] *= S.info[at][g].rest;
-      }
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) pw[g][j] = (E)sc[g / 2][8 * (g % 2) + j];
       // one multiply after the other into different sums: into the same one it would wait
 #pragma unroll
       for (int g = 0; g < 4; ++g)
@@ -1129,6 +1116,27 @@ struct Plan {
   int64_t splits, chunk, blocks;
 };
 
+// Splits of many rows whose spans are alike, up to `most`: those of the least
+// time by what was measured at 128 channels.  A tile takes a block 1.9 us where
+// it has its unit to itself, 2.5 where two share one; splits cost 8 us, and
+// their partial sums, written and read, go at 4 TB/s.  (42 heads of 128 over 6,
+// 768 new tokens: 16 tiles 44 us whole and 59 halved, 66 tiles 127 and 115; 18
+// new tokens 75 whole, 28 in four.)
+int64_t many_splits(int64_t tiles, int64_t base, int64_t most, int64_t dim) {
+  int64_t best = 1;
+  double least = 0.0;
+  for (int64_t n = 1; n <= most; ++n) {
+    const double tile = (n * base <= 256 ? 1.9 : 2.5) * (double)dim / 128;
+    const double sums = n == 1 ? 0.0 : 8.0 + (double)(n * base * kManyRows * dim * 8) / 4e6;
+    const double time = (double)((tiles + n - 1) / n) * tile + sums;
+    if (n == 1 || time < least) {
+      best = n;
+      least = time;
+    }
+  }
+  return best;
+}
+
 Plan make_plan(int64_t heads_q, int64_t heads, int64_t page, int64_t batch, int64_t max_q, int64_t width,
                int64_t window, int64_t sinks, nvfp4_dtype_t dt, int64_t dim, bool split) {
   Plan p;
@@ -1161,6 +1169,7 @@ Plan make_plan(int64_t heads_q, int64_t heads, int64_t page, int64_t batch, int6
     int64_t want = full / base;
     const int64_t most = (tiles + least - 1) / least;
     if (want > most) want = most;
+    if (p.many && alike) want = many_splits(tiles, base, want, dim);
     if (want > 1) {
       p.chunk = ((tiles + want - 1) / want + unit - 1) / unit * unit * 64;
       p.splits = (tiles * 64 + p.chunk - 1) / p.chunk;

@@ -21,7 +21,7 @@ from typing import Optional
 
 import torch
 
-from . import NVFP4Error, _check, _dtype_code, _on_device, _stream, load_library
+from . import _CURRENT_DEVICE, NVFP4Error, _check, _dtype_code, _stream, load_library
 
 _PAGES = (16, 32, 64, 128, 256)
 _DIMS = (64, 128, 192, 256)
@@ -189,6 +189,9 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, table: torch.Ten
     weight.
     """
     dtype, shape, index, dim = k.dtype, k.shape, cache._index, cache._dim
+    if _CURRENT_DEVICE() != index:
+        with torch.cuda.device(index):
+            return kv_append(k, v, cache, table, lens, q, cu_q, max_q, inv_freq, interleaved, out, q_norm, k_norm, eps)
     code = _dtype_code(dtype)
     tokens = shape[0] if len(shape) else 0
     want = (tokens, cache._heads, dim)
@@ -233,14 +236,22 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, table: torch.Ten
         return out
     if heads_q == 0:
         qp = qo = qn = None      # a tensor without heads has no address
-    _check("nvfp4_kv_append_norm", _on_device(
-        cache._index, load_library().nvfp4_kv_append_norm, cache._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0],
-        vs[1], qp, q_token, q_head, heads_q, qo, code, tokens, cu, batch, most, table.data_ptr(), width, lens.data_ptr(),
-        freq, rot, 1 if interleaved else 0, qn, qn_head, kn, kn_head, eps, _stream(cache._device)))
+    lib = load_library()
+    if qn is None and kn is None:
+        _check("nvfp4_kv_append", lib.nvfp4_kv_append(
+            cache._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], qp, q_token, q_head, heads_q, qo, code,
+            tokens, cu, batch, most, table.data_ptr(), width, lens.data_ptr(), freq, rot, 1 if interleaved else 0,
+            _stream(cache._device)))
+    else:
+        _check("nvfp4_kv_append_norm", lib.nvfp4_kv_append_norm(
+            cache._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], qp, q_token, q_head, heads_q, qo, code,
+            tokens, cu, batch, most, table.data_ptr(), width, lens.data_ptr(), freq, rot, 1 if interleaved else 0,
+            qn, qn_head, kn, kn_head, eps, _stream(cache._device)))
     return out
 
 
 # nvfp4_paged_attention_workspace_size by call shape, as for qmm's workspace
+# (keys with sinks are one longer)
 _ATTENTION_WS_CACHE: dict = {}
 
 
@@ -257,6 +268,9 @@ def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
     sees are not read.  scale defaults to dim ** -0.5.  Returns [tokens, heads,
     dim] in q's dtype, zeros for a query that sees nothing.
     """
+    if _CURRENT_DEVICE() != cache._index:
+        with torch.cuda.device(cache._index):
+            return paged_attention(q, cache, table, lens, cu_q, max_q, window, scale, out, sinks)
     code = _dtype_code(q.dtype)
     shape, heads, dim = q.shape, cache._heads, cache._dim
     tokens, heads_q = (shape[0], shape[1]) if len(shape) == 3 else (0, 0)
@@ -271,19 +285,23 @@ def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
     if tokens == 0 or heads_q == 0:
         return out
     lib = load_library()
-    key = (tokens, heads_q, heads, dim, cache._page, batch, most, width, window, sinks, code)
+    if sinks > 0 and window > 0:
+        fn, seen = "nvfp4_paged_attention_sinks", (window, sinks)
+    else:
+        fn, seen = "nvfp4_paged_attention", (window,)
+    key = (tokens, heads_q, heads, dim, cache._page, batch, most, width, *seen, code)
     ws_bytes = _ATTENTION_WS_CACHE.get(key)
     if ws_bytes is None:
-        ws_bytes = int(lib.nvfp4_paged_attention_sinks_workspace_size(*key))
+        ws_bytes = int(getattr(lib, fn + "_workspace_size")(*key))
         if ws_bytes < 0:
-            raise NVFP4Error("nvfp4_paged_attention_sinks_workspace_size", ws_bytes)
+            raise NVFP4Error(fn + "_workspace_size", ws_bytes)
         if len(_ATTENTION_WS_CACHE) < 4096:
             _ATTENTION_WS_CACHE[key] = ws_bytes
     ws = torch.empty(ws_bytes, dtype=_U8, device=cache._device) if ws_bytes else None
-    _check("nvfp4_paged_attention_sinks", _on_device(
-        cache._index, lib.nvfp4_paged_attention_sinks, cache._ref, q.data_ptr(), qs[0], qs[1], heads_q, code, tokens, cu,
-        batch, most, table.data_ptr(), width, lens.data_ptr(), window, sinks, dim ** -0.5 if scale is None else scale,
-        ws.data_ptr() if ws_bytes else None, ws_bytes, out.data_ptr(), _stream(cache._device)))
+    _check(fn, getattr(lib, fn)(
+        cache._ref, q.data_ptr(), qs[0], qs[1], heads_q, code, tokens, cu, batch, most, table.data_ptr(), width,
+        lens.data_ptr(), *seen, dim ** -0.5 if scale is None else scale, ws.data_ptr() if ws_bytes else None, ws_bytes,
+        out.data_ptr(), _stream(cache._device)))
     return out
 
 

@@ -56,7 +56,6 @@ def test_attention_workspace(lib):  # noqa: F811
             assert size(*sizes, window, 0, BF16) == size(*sizes, window, -5, BF16) == plain(*sizes, window, BF16)
             assert size(*sizes, window, 1 << 50, BF16) >= 0
         assert size(*sizes, 0, 500, BF16) == plain(*sizes, 0, BF16)           # no window: the sinks say nothing
-        assert size(*sizes, 100, 1 << 50, BF16) == plain(*sizes, 0, BF16)     # all are sinks: as long as without a window
     assert size(1, 32, 8, 128, 48, 1, 1, 2000, 100, 4, BF16) == UNSUP
     assert size(1, 31, 8, 128, 64, 1, 1, 2000, 100, 4, BF16) == SHAPE
     assert size(1, 32, 8, 128, 64, 1, 1, 2000, 100, 4, 3) == DTYPE
