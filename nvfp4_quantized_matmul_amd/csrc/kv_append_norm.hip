@@ -24,8 +24,6 @@ using namespace nvfp4dev;
 // Rounds of a page's keys that stay in registers between the two passes over
 // it; what is over is formed twice.
 constexpr int kHeld = 4;
-// Rounds of queries that are loaded ahead.
-constexpr int kAhead = 2;
 
 // W = 8, 4 or 1 consecutive elements as they are loaded.
 template <typename T, int W>
@@ -324,18 +322,17 @@ __device__ void norm_queries(const AppendArgs& A, int64_t block, int q_heads, in
   constexpr int ITEMS = Row<T, W, INTER>::kItems;
   Row<T, W, INTER> row(A);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t unit = block * (THREADS / 64) + wave;
-  const int64_t t = unit / q_parts;
-  const int h0 = (int)(unit - t * q_parts) * q_heads, each = 64 / row.lanes, mine = lane / row.lanes;
+  // a grid has less than 2^26 waves
+  const uint32_t unit = (uint32_t)block * (THREADS / 64) + (uint32_t)wave, token = unit / (uint32_t)q_parts;
+  const int64_t t = token;
+  const int h0 = (int)(unit - token * (uint32_t)q_parts) * q_heads, each = 64 / row.lanes, mine = lane / row.lanes;
   const int h1 = h0 + q_heads < A.heads_q ? h0 + q_heads : A.heads_q;
   const bool there = t < A.s.tokens;
   turn += wave * 128;   // half of a row of 256 channels
-  RowData<T, W> x[kAhead];
+  RowData<T, W> x;
   const T* q = (const T*)A.q + (there ? t : 0) * A.q_token;
   const auto load = [&](int h, RowData<T, W>& x) { x.load(row, q + (int64_t)(h < h1 ? h : h1 - 1) * A.q_head); };
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) load(h0 + i * each + mine, x[i]);
-  // weights of a head each are loaded a round ahead as well
+  load(h0 + mine, x);
   const auto load_weights = [&](int h, Weights<W, ITEMS>& w) { w.load(row, A.q_norm + (h < h1 ? h : h1 - 1) * A.q_norm_head); };
   Weights<W, ITEMS> weights;
   if (A.q_norm) load_weights(h0 + mine, weights);
@@ -344,7 +341,7 @@ __device__ void norm_queries(const AppendArgs& A, int64_t block, int q_heads, in
   for (int f = lane; f < A.rot / 2; f += 64) {
     double sn, cs;
     sin_cos(at * (double)A.inv_freq[f], &sn, &cs);
-    turn[f] = make_double2(sn, cs);
+    turn[f % W * row.turning + f / W] = make_double2(sn, cs);   // the lanes' pairs i side by side: no bank twice
   }
   // a wave reads what it wrote itself: in order, if the compiler keeps it
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -352,13 +349,11 @@ __device__ void norm_queries(const AppendArgs& A, int64_t block, int q_heads, in
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   if (p == kLeftOut) return;
   for (int h = h0; h < h1; h += each) {
-    Weights<W, ITEMS> w = weights;
-    if (A.q_norm_head != 0) load_weights(h + each + mine, weights);
     float a[ITEMS][W], b[ITEMS][W];
-    norm_row<T, W, INTER>(A, row, x[0], w, A.q_norm != nullptr, [&](int r, int i) { return turn[W * row.item[r] + i]; }, a, b);
-#pragma unroll
-    for (int i = 0; i + 1 < kAhead; ++i) x[i] = x[i + 1];
-    load(h + kAhead * each + mine, x[kAhead - 1]);
+    norm_row<T, W, INTER>(A, row, x, weights, A.q_norm != nullptr, [&](int r, int i) { return turn[i * row.turning + row.item[r]]; }, a, b);
+    // the next round's, behind the last one that one's again
+    load(h + each + mine, x);
+    if (A.q_norm_head != 0) load_weights(h + each + mine, weights);
     if (row.active && h + mine < h1) {
       T* out = (T*)A.q_out + (t * A.heads_q + h + mine) * A.dim;
 #pragma unroll
