@@ -341,6 +341,8 @@ __global__ __launch_bounds__(kPlan) void compact_kernel(CompactArgs A) {
 // copying
 // ---------------------------------------------------------------------------
 
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
 struct CopyArgs {
   const int32_t* copies;
   int64_t page_bytes;       // of a side
@@ -352,6 +354,14 @@ struct CopyArgs {
 };
 
 // A row of blocks for each cache and side, and one for the table.
+//
+// Bound by memory.  Copies are not read again soon, so they are stored past the
+// caches, and with ONCE, where each page is copied to one other alone, loaded
+// past them too: half of a pool of 2048 pages compacted in 4 layers (537 MB,
+// read and written) 109 us with the plan, 4.9 TB/s, 124 through the caches; 64
+// copies of 8 pages in 16 layers (268 MB) 41 us with stores alone past them, 63
+// through, 58 with loads past them as well.
+template <bool ONCE>
 __global__ __launch_bounds__(kThreads) void copy_kernel(CopyArgs A) {
   const int layer = blockIdx.y >> 1, side = blockIdx.y & 1;
   if (layer == A.layers) {
@@ -367,16 +377,18 @@ __global__ __launch_bounds__(kThreads) void copy_kernel(CopyArgs A) {
   for (uint32_t at = blockIdx.x; at < all; at += gridDim.x) {
     const uint32_t pair = at / (uint32_t)A.pieces, piece = at - pair * (uint32_t)A.pieces;
     const int64_t from = A.copies[4 + 2 * pair], to = A.copies[5 + 2 * pair];
-    const uint4* src = (const uint4*)(base + from * A.page_bytes);
-    uint4* dst = (uint4*)(base + to * A.page_bytes);
+    const u32x4_t* src = (const u32x4_t*)(base + from * A.page_bytes);
+    u32x4_t* dst = (u32x4_t*)(base + to * A.page_bytes);
     const int64_t vecs = A.page_bytes / 16, first = (int64_t)piece * (kPiece / 16) + threadIdx.x;
-    uint4 x[kVecs];
+    u32x4_t x[kVecs];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const u32x4_t* at = src + first + i * kThreads;
+      if (first + i * kThreads < vecs) x[i] = ONCE ? __builtin_nontemporal_load(at) : *at;
+    }
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
-      if (first + i * kThreads < vecs) x[i] = src[first + i * kThreads];
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i)
-      if (first + i * kThreads < vecs) dst[first + i * kThreads] = x[i];
+      if (first + i * kThreads < vecs) __builtin_nontemporal_store(x[i], dst + first + i * kThreads);
     if (piece == 0) {
       uint8_t* scales = side ? A.vs[layer] : A.ks[layer];
       for (int h = threadIdx.x; h < A.heads; h += kThreads) scales[to * A.heads + h] = scales[from * A.heads + h];
@@ -386,6 +398,7 @@ __global__ __launch_bounds__(kThreads) void copy_kernel(CopyArgs A) {
 
 int64_t blocks_of(int64_t cells) { return (cells + kCells - 1) / kCells; }
 
+template <bool ONCE>
 void launch_copies(const nvfp4_kv_cache_t* caches, int64_t count, const int32_t* copies, int64_t most, int32_t* table,
                    const int32_t* where, int64_t cells, hipStream_t s) {
   CopyArgs A;
@@ -407,7 +420,7 @@ void launch_copies(const nvfp4_kv_cache_t* caches, int64_t count, const int32_t*
     const int64_t row = std::max<int64_t>(kCopyBlocks / (2 * A.layers), 1);
     int64_t x = most < row ? std::min(row, most * std::min<int64_t>(A.pieces, row)) : row;
     if (rewrite) x = std::max(x, std::min(blocks_of(cells), row));
-    if (x > 0) copy_kernel<<<dim3((uint32_t)x, (uint32_t)(2 * A.layers + (rewrite ? 1 : 0))), dim3(kThreads), 0, s>>>(A);
+    if (x > 0) copy_kernel<ONCE><<<dim3((uint32_t)x, (uint32_t)(2 * A.layers + (rewrite ? 1 : 0))), dim3(kThreads), 0, s>>>(A);
   }
 }
 
@@ -454,14 +467,14 @@ void launch_kv_reserve(const nvfp4_kv_cache_t* caches, int64_t count, int32_t* t
   A.page_shift = __builtin_ctz((unsigned)caches->page);
   A.vec = aligned16(refs);
   reserve_kernel<<<dim3(1), dim3(kPlan), 0, s>>>(A);
-  launch_copies(caches, count, A.copies, batch, nullptr, nullptr, 0, s);
+  launch_copies<false>(caches, count, A.copies, batch, nullptr, nullptr, 0, s);
 }
 
 void launch_kv_compact(const nvfp4_kv_cache_t* caches, int64_t count, int32_t* table, int64_t batch, int64_t width,
                        int32_t* refs, void* ws, int32_t* used, int32_t* where, hipStream_t s) {
   const CompactArgs A = {refs, used, where, (int32_t*)ws, (int32_t)caches->pages, aligned16(refs)};
   compact_kernel<<<dim3(1), dim3(kPlan), 0, s>>>(A);
-  launch_copies(caches, count, A.copies, caches->pages / 2, table, where, batch * width, s);
+  launch_copies<true>(caches, count, A.copies, caches->pages / 2, table, where, batch * width, s);
 }
 
 }  // namespace nvfp4host
