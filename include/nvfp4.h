@@ -599,7 +599,7 @@ int nvfp4_kv_free(int32_t* table, int64_t batch, int64_t width, const int32_t* l
  * workspace: device, 16-byte aligned, of at least
  * nvfp4_kv_reserve_workspace_size bytes.
  */
-int64_t nvfp4_kv_reserve_workspace_size(int64_t tokens, int64_t batch, int64_t page);
+int64_t nvfp4_kv_reserve_workspace_size(int64_t tokens, int64_t batch, int64_t page, int64_t pages);
 int nvfp4_kv_reserve(const nvfp4_kv_cache_t* caches, int64_t count, int32_t* table, int64_t batch, int64_t width,
                      const int32_t* lens, const int32_t* cu_q, int64_t tokens, int32_t* refs, void* workspace,
                      int64_t workspace_bytes, int32_t* missing, hipStream_t stream);

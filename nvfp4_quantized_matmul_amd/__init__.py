@@ -94,7 +94,7 @@ def load_library() -> ctypes.CDLL:
         "nvfp4_sample_workspace_size": [i64, i64, c_int],
         "nvfp4_sample": [vp, c_int, i64, i64, i64, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp],
         "nvfp4_kv_free": [vp, i64, i64, vp, i64, i64, i64, vp, i64, vp],
-        "nvfp4_kv_reserve_workspace_size": [i64, i64, i64],
+        "nvfp4_kv_reserve_workspace_size": [i64, i64, i64, i64],
         "nvfp4_kv_reserve": [vp, i64, vp, i64, i64, vp, vp, i64, vp, vp, i64, vp, vp],
         "nvfp4_kv_fork": [vp, i64, i64, vp, vp, i64, vp, i64, vp, vp, vp],
         "nvfp4_kv_compact_workspace_size": [i64],

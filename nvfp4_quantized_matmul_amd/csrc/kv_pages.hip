@@ -21,8 +21,12 @@ using namespace nvfp4dev;
 constexpr int kThreads = 256;
 // Cells of the table that a block takes.
 constexpr int kCells = 4 * kThreads;
-// Threads of the block that plans, and pages that a thread looks at in a round.
-constexpr int kPlan = 1024, kScan = 16;
+// Threads of a block that plans, pages that a thread looks at in a round, and
+// those of a round of all of them.
+constexpr int kPlan = 1024, kScan = 16, kRound = kPlan * kScan;
+// Pools of more pages than these are counted by a launch of many blocks before
+// they are planned: one block takes 1.5 us a round.
+constexpr int64_t kReserveAlone = 4 * kRound, kCompactAlone = kRound;
 // Bytes of a page's side that a block copies at a time, in 16-byte accesses.
 constexpr int kVecs = 4, kPiece = kVecs * kThreads * 16;
 // Caches of a copying launch: their addresses are its arguments.
@@ -71,6 +75,20 @@ __device__ __forceinline__ uint32_t free_pages(const int32_t* refs, int64_t p, i
 #pragma unroll
   for (int i = 0; i < kScan; ++i) m |= r[i] <= 0 ? 1u << i : 0u;
   return m;
+}
+
+// The pages of a thread's kScan from p on that are there, and those below `end`.
+__device__ __forceinline__ uint32_t pages_below(int64_t p, int64_t end) {
+  return p >= end ? 0 : end - p < kScan ? (1u << (end - p)) - 1 : (1u << kScan) - 1;
+}
+
+// The free pages of each round.
+__global__ __launch_bounds__(kPlan) void count_kernel(const int32_t* refs, int32_t* counts, int32_t pages, bool vec) {
+  __shared__ int shared[kPlan / 64];
+  const int64_t p = (int64_t)blockIdx.x * kRound + threadIdx.x * kScan;
+  int all;
+  block_scan(__popc(free_pages(refs, p, pages, vec)), shared, &all);
+  if (threadIdx.x == 0) counts[blockIdx.x] = all;
 }
 
 // ---------------------------------------------------------------------------
@@ -161,6 +179,7 @@ struct ReserveArgs {
   int32_t* copies;    // their number, and from [4] on the pairs (from, to)
   int32_t* ranks;     // [items + 1]: needs before an item
   int32_t* fresh;     // [items]: the pages taken, from rank kPlan on
+  const int32_t* counts;   // free pages of each round, or null: not counted
   int32_t items, pages, page_shift;
   bool vec;           // 16-byte loads of refs
 };
@@ -235,8 +254,8 @@ __global__ __launch_bounds__(kPlan) void reserve_kernel(ReserveArgs A) {
 
   // the first `want` free pages
   int have = 0;
-  for (int64_t p0 = 0; p0 < A.pages && have < want; p0 += kPlan * kScan) {
-    const int64_t p = p0 + tid * kScan;
+  const auto take = [&](int64_t round) {
+    const int64_t p = round * kRound + tid * kScan;
     uint32_t m = free_pages(A.refs, p, A.pages, A.vec);
     int all, rank = have + block_scan(__popc(m), shared, &all);
     for (; m && rank < want; m &= m - 1, ++rank) {
@@ -244,6 +263,17 @@ __global__ __launch_bounds__(kPlan) void reserve_kernel(ReserveArgs A) {
       if (rank < kPlan) fresh[rank] = id; else A.fresh[rank] = id;
     }
     have += all;
+  };
+  const int64_t rounds = ((int64_t)A.pages + kRound - 1) / kRound;
+  if (!A.counts) {
+    for (int64_t r = 0; r < rounds && have < want; ++r) take(r);
+  } else {
+    // only rounds with free pages, 64 of them looked up at a time
+    for (int64_t r0 = 0; r0 < rounds && have < want; r0 += 64) {
+      const int64_t r = r0 + (tid & 63);
+      uint64_t some = __ballot(r < rounds && A.counts[r] > 0);
+      for (; some && have < want; some &= some - 1) take(r0 + __builtin_ctzll(some));
+    }
   }
   __syncthreads();
 
@@ -283,7 +313,7 @@ __global__ __launch_bounds__(kPlan) void reserve_kernel(ReserveArgs A) {
 }
 
 // ---------------------------------------------------------------------------
-// compacting: one block plans
+// compacting: one block plans, or a block each round
 // ---------------------------------------------------------------------------
 
 struct CompactArgs {
@@ -293,48 +323,83 @@ struct CompactArgs {
   bool vec;
 };
 
+// The round's part of the plan: holes are the free pages below `used`, movers
+// the pages in use from there on; `holes` and `movers` count those of earlier
+// rounds.
+__device__ __forceinline__ void plan_round(const CompactArgs& A, int64_t round, int used, int* holes, int* movers, int* shared) {
+  const int64_t p = round * kRound + threadIdx.x * kScan;
+  const uint32_t inside = pages_below(p, A.pages), low = pages_below(p, used);
+  const uint32_t empty = free_pages(A.refs, p, A.pages, A.vec) & inside;
+  uint32_t hole = empty & low, mover = inside & ~empty & ~low;
+#pragma unroll
+  for (int i = 0; i < kScan; ++i)
+    if ((inside >> i) & 1) A.where[p + i] = (empty >> i) & 1 ? -1 : (int32_t)(p + i);
+  int sum;   // a round has at most 2^14 of each
+  const int before = block_scan(__popc(hole) | (__popc(mover) << 16), shared, &sum);
+  for (int k = *holes + (before & 0xffff); hole; hole &= hole - 1, ++k) A.copies[5 + 2 * (int64_t)k] = (int32_t)(p + __builtin_ctz(hole));
+  for (int k = *movers + (before >> 16); mover; mover &= mover - 1, ++k) A.copies[4 + 2 * (int64_t)k] = (int32_t)(p + __builtin_ctz(mover));
+  *holes += sum & 0xffff;
+  *movers += sum >> 16;
+}
+
+__device__ __forceinline__ void move_count(const CompactArgs& A, int64_t k) {
+  const int32_t from = A.copies[4 + 2 * k], to = A.copies[5 + 2 * k];
+  A.where[from] = to;
+  A.refs[to] = A.refs[from];
+  A.refs[from] = 0;
+}
+
 __global__ __launch_bounds__(kPlan) void compact_kernel(CompactArgs A) {
   __shared__ int shared[kPlan / 64];
   const int tid = threadIdx.x;
-  constexpr int kRound = kPlan * kScan;
+  const int64_t rounds = ((int64_t)A.pages + kRound - 1) / kRound;
   int used = 0;
-  for (int64_t p0 = 0; p0 < A.pages; p0 += kRound) {
-    const int64_t p = p0 + tid * kScan;
-    const int64_t n = p < A.pages ? (A.pages - p < kScan ? A.pages - p : kScan) : 0;
-    used += (int)n - __popc(free_pages(A.refs, p, A.pages, A.vec));
+  for (int64_t r = 0; r < rounds; ++r) {
+    const int64_t p = r * kRound + tid * kScan;
+    used += __popc(pages_below(p, A.pages)) - __popc(free_pages(A.refs, p, A.pages, A.vec));
   }
   int all;
   block_scan(used, shared, &all);
   used = all;
-  // holes below `used` and pages in use from there on: the k-th of these goes to the k-th of those
   int holes = 0, movers = 0;
-  for (int64_t p0 = 0; p0 < A.pages; p0 += kRound) {
-    const int64_t p = p0 + tid * kScan;
-    const uint32_t inside = p >= A.pages ? 0 : A.pages - p < kScan ? (1u << (A.pages - p)) - 1 : (1u << kScan) - 1;
-    const uint32_t low = p >= used ? 0 : used - p < kScan ? (1u << (used - p)) - 1 : (1u << kScan) - 1;
-    const uint32_t empty = free_pages(A.refs, p, A.pages, A.vec) & inside;
-    uint32_t hole = empty & low, mover = inside & ~empty & ~low;
-#pragma unroll
-    for (int i = 0; i < kScan; ++i)
-      if ((inside >> i) & 1) A.where[p + i] = (empty >> i) & 1 ? -1 : (int32_t)(p + i);
-    int sum;   // a round has at most 2^14 of each
-    const int before = block_scan(__popc(hole) | (__popc(mover) << 16), shared, &sum);
-    for (int k = holes + (before & 0xffff); hole; hole &= hole - 1, ++k) A.copies[5 + 2 * k] = (int32_t)(p + __builtin_ctz(hole));
-    for (int k = movers + (before >> 16); mover; mover &= mover - 1, ++k) A.copies[4 + 2 * k] = (int32_t)(p + __builtin_ctz(mover));
-    holes += sum & 0xffff;
-    movers += sum >> 16;
-  }
+  for (int64_t r = 0; r < rounds; ++r) plan_round(A, r, used, &holes, &movers, shared);
   __syncthreads();
-  for (int k = tid; k < movers; k += kPlan) {
-    const int32_t from = A.copies[4 + 2 * k], to = A.copies[5 + 2 * k];
-    A.where[from] = to;
-    A.refs[to] = A.refs[from];
-    A.refs[from] = 0;
-  }
+  for (int k = tid; k < movers; k += kPlan) move_count(A, k);
   if (tid == 0) {
     A.copies[0] = movers;
     *A.used = used;
   }
+}
+
+// The same by a block each round, with the rounds' free pages counted.
+__global__ __launch_bounds__(kPlan) void compact_round_kernel(CompactArgs A, const int32_t* counts) {
+  __shared__ int shared[kPlan / 64];
+  const int rounds = (int)(((int64_t)A.pages + kRound - 1) / kRound);
+  const auto sum_to = [&](int end) {
+    int v = 0, all;
+    for (int r = threadIdx.x; r < end; r += kPlan) v += counts[r];
+    block_scan(v, shared, &all);
+    return all;
+  };
+  const int used = A.pages - sum_to(rounds), mine = (int)blockIdx.x, border = used / kRound;
+  // the holes before this round and all of them: the free pages below `used`
+  const int64_t p = (int64_t)border * kRound + threadIdx.x * kScan;
+  int in_border;
+  block_scan(__popc(free_pages(A.refs, p, A.pages, A.vec) & pages_below(p, used)), shared, &in_border);
+  const int all = sum_to(border < rounds ? border : rounds) + in_border, free_before = sum_to(mine);
+  // the movers before this round: pages in use before it but for those below `used`
+  int holes = mine <= border ? free_before : all;
+  int movers = mine <= border ? 0 : mine * kRound - free_before - (used - all);
+  if (mine == 0 && threadIdx.x == 0) {
+    A.copies[0] = all;
+    *A.used = used;
+  }
+  plan_round(A, mine, used, &holes, &movers, shared);
+}
+
+__global__ __launch_bounds__(kThreads) void move_counts_kernel(CompactArgs A) {
+  const int64_t k = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (k < A.copies[0]) move_count(A, k);
 }
 
 // ---------------------------------------------------------------------------
@@ -346,7 +411,8 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 struct CopyArgs {
   const int32_t* copies;
   int64_t page_bytes;       // of a side
-  int32_t heads, layers, pieces;
+  int32_t heads, layers;
+  int32_t pieces, group;    // pieces of a page, or the pages that fit one
   int32_t* table;           // to be rewritten by `where`, by the last row of blocks
   const int32_t* where;
   int32_t cells, pages;
@@ -360,8 +426,9 @@ struct CopyArgs {
 // past them too: half of a pool of 2048 pages compacted in 4 layers (537 MB,
 // read and written) 109 us with the plan, 4.9 TB/s, 124 through the caches; 64
 // copies of 8 pages in 16 layers (268 MB) 41 us with stores alone past them, 63
-// through, 58 with loads past them as well.
-template <bool ONCE>
+// through, 58 with loads past them as well.  GROUPED: a block copies several
+// small pages at a time.
+template <bool ONCE, bool GROUPED>
 __global__ __launch_bounds__(kThreads) void copy_kernel(CopyArgs A) {
   const int layer = blockIdx.y >> 1, side = blockIdx.y & 1;
   if (layer == A.layers) {
@@ -372,26 +439,49 @@ __global__ __launch_bounds__(kThreads) void copy_kernel(CopyArgs A) {
     return;
   }
   // pieces of all pages of a pool of 2^31 pages would pass 32 bits, those of one in memory do not
-  const uint32_t all = (uint32_t)A.copies[0] * (uint32_t)A.pieces;
+  const uint32_t count = (uint32_t)A.copies[0], vecs = (uint32_t)(A.page_bytes / 16), heads = (uint32_t)A.heads;
+  const uint32_t group = GROUPED ? (uint32_t)A.group : 1, all = (count + group - 1) / group * (uint32_t)A.pieces;
   uint8_t* const base = side ? A.v[layer] : A.k[layer];
+  uint8_t* const scales = side ? A.vs[layer] : A.ks[layer];
   for (uint32_t at = blockIdx.x; at < all; at += gridDim.x) {
-    const uint32_t pair = at / (uint32_t)A.pieces, piece = at - pair * (uint32_t)A.pieces;
-    const int64_t from = A.copies[4 + 2 * pair], to = A.copies[5 + 2 * pair];
-    const u32x4_t* src = (const u32x4_t*)(base + from * A.page_bytes);
-    u32x4_t* dst = (u32x4_t*)(base + to * A.page_bytes);
-    const int64_t vecs = A.page_bytes / 16, first = (int64_t)piece * (kPiece / 16) + threadIdx.x;
+    const uint32_t first = GROUPED ? at : at / (uint32_t)A.pieces, piece = at - first * (uint32_t)A.pieces, pair0 = first * group;
+    const int64_t from0 = A.copies[4 + 2 * (int64_t)pair0], to0 = A.copies[5 + 2 * (int64_t)pair0];
     u32x4_t x[kVecs];
+    if constexpr (!GROUPED) {
+      const u32x4_t* src = (const u32x4_t*)(base + from0 * A.page_bytes);
+      u32x4_t* dst = (u32x4_t*)(base + to0 * A.page_bytes);
+      const uint32_t v = piece * (kPiece / 16) + threadIdx.x;
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const u32x4_t* at = src + first + i * kThreads;
-      if (first + i * kThreads < vecs) x[i] = ONCE ? __builtin_nontemporal_load(at) : *at;
+      for (int i = 0; i < kVecs; ++i)
+        if (v + i * kThreads < vecs) x[i] = ONCE ? __builtin_nontemporal_load(src + v + i * kThreads) : src[v + i * kThreads];
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i)
+        if (v + i * kThreads < vecs) __builtin_nontemporal_store(x[i], dst + v + i * kThreads);
+    } else {
+      u32x4_t* dst[kVecs];
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        const uint32_t v = i * kThreads + threadIdx.x, local = v / vecs, off = v - local * vecs, pair = pair0 + local;
+        dst[i] = nullptr;
+        if (local < group && pair < count) {
+          const int64_t from = A.copies[4 + 2 * (int64_t)pair], to = A.copies[5 + 2 * (int64_t)pair];
+          const u32x4_t* src = (const u32x4_t*)(base + from * A.page_bytes) + off;
+          dst[i] = (u32x4_t*)(base + to * A.page_bytes) + off;
+          x[i] = ONCE ? __builtin_nontemporal_load(src) : *src;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i)
+        if (dst[i]) __builtin_nontemporal_store(x[i], dst[i]);
     }
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i)
-      if (first + i * kThreads < vecs) __builtin_nontemporal_store(x[i], dst + first + i * kThreads);
     if (piece == 0) {
-      uint8_t* scales = side ? A.vs[layer] : A.ks[layer];
-      for (int h = threadIdx.x; h < A.heads; h += kThreads) scales[to * A.heads + h] = scales[from * A.heads + h];
+      for (uint32_t h = threadIdx.x; h < heads * group; h += kThreads) {
+        const uint32_t local = GROUPED ? h / heads : 0, pair = pair0 + local, head = h - local * heads;
+        if (pair < count) {
+          const int64_t from = A.copies[4 + 2 * (int64_t)pair], to = A.copies[5 + 2 * (int64_t)pair];
+          scales[to * heads + head] = scales[from * heads + head];
+        }
+      }
     }
   }
 }
@@ -407,6 +497,7 @@ void launch_copies(const nvfp4_kv_cache_t* caches, int64_t count, const int32_t*
   A.heads = (int32_t)caches->heads;
   A.pages = (int32_t)caches->pages;
   A.pieces = (int32_t)((A.page_bytes + kPiece - 1) / kPiece);
+  A.group = (int32_t)std::max<int64_t>(kPiece / A.page_bytes, 1);
   A.table = table;
   A.where = where;
   A.cells = (int32_t)cells;
@@ -418,13 +509,18 @@ void launch_copies(const nvfp4_kv_cache_t* caches, int64_t count, const int32_t*
       A.k[i] = c.k; A.v[i] = c.v; A.ks[i] = c.k_scales; A.vs[i] = c.v_scales;
     }
     const int64_t row = std::max<int64_t>(kCopyBlocks / (2 * A.layers), 1);
-    int64_t x = most < row ? std::min(row, most * std::min<int64_t>(A.pieces, row)) : row;
+    const int64_t groups = (most + A.group - 1) / A.group;
+    int64_t x = groups < row ? std::min(row, groups * std::min<int64_t>(A.pieces, row)) : row;
     if (rewrite) x = std::max(x, std::min(blocks_of(cells), row));
-    if (x > 0) copy_kernel<ONCE><<<dim3((uint32_t)x, (uint32_t)(2 * A.layers + (rewrite ? 1 : 0))), dim3(kThreads), 0, s>>>(A);
+    const dim3 grid((uint32_t)x, (uint32_t)(2 * A.layers + (rewrite ? 1 : 0)));
+    if (x > 0 && A.group > 1) copy_kernel<ONCE, true><<<grid, dim3(kThreads), 0, s>>>(A);
+    else if (x > 0) copy_kernel<ONCE, false><<<grid, dim3(kThreads), 0, s>>>(A);
   }
 }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+int64_t rounds_of(int64_t pages) { return (pages + kRound - 1) / kRound; }
 
 }  // namespace
 
@@ -434,9 +530,13 @@ int64_t kv_reserve_items(int64_t tokens, int64_t batch, int64_t page, bool offse
   return offsets ? tokens / page + 2 * batch : batch;
 }
 
-int64_t kv_reserve_bytes(int64_t items, int64_t batch) { return ((4 + 2 * batch + 2 * items + 1) * 4 + 255) / 256 * 256; }
+// The copies and their number, ranks, pages taken, the rounds' free pages.
+int64_t kv_reserve_bytes(int64_t items, int64_t batch, int64_t pages) {
+  return ((4 + 2 * batch + 2 * items + 1 + (pages > kReserveAlone ? rounds_of(pages) : 0)) * 4 + 255) / 256 * 256;
+}
 
-int64_t kv_compact_bytes(int64_t pages) { return ((4 + pages + 1) * 4 + 255) / 256 * 256; }
+// The copies and their number, the rounds' free pages.
+int64_t kv_compact_bytes(int64_t pages) { return ((4 + pages + 1 + rounds_of(pages)) * 4 + 255) / 256 * 256; }
 
 void launch_kv_free(int32_t* table, int64_t batch, int64_t width, const int32_t* lens, int64_t page, int64_t keep,
                     int64_t sinks, int32_t* refs, int64_t pages, hipStream_t s) {
@@ -466,6 +566,12 @@ void launch_kv_reserve(const nvfp4_kv_cache_t* caches, int64_t count, int32_t* t
   A.items = (int32_t)items; A.pages = (int32_t)caches->pages;
   A.page_shift = __builtin_ctz((unsigned)caches->page);
   A.vec = aligned16(refs);
+  A.counts = nullptr;
+  if (caches->pages > kReserveAlone) {
+    int32_t* counts = A.fresh + items;
+    count_kernel<<<dim3((uint32_t)rounds_of(caches->pages)), dim3(kPlan), 0, s>>>(refs, counts, A.pages, A.vec);
+    A.counts = counts;
+  }
   reserve_kernel<<<dim3(1), dim3(kPlan), 0, s>>>(A);
   launch_copies<false>(caches, count, A.copies, batch, nullptr, nullptr, 0, s);
 }
@@ -473,7 +579,15 @@ void launch_kv_reserve(const nvfp4_kv_cache_t* caches, int64_t count, int32_t* t
 void launch_kv_compact(const nvfp4_kv_cache_t* caches, int64_t count, int32_t* table, int64_t batch, int64_t width,
                        int32_t* refs, void* ws, int32_t* used, int32_t* where, hipStream_t s) {
   const CompactArgs A = {refs, used, where, (int32_t*)ws, (int32_t)caches->pages, aligned16(refs)};
-  compact_kernel<<<dim3(1), dim3(kPlan), 0, s>>>(A);
+  if (caches->pages <= kCompactAlone) {
+    compact_kernel<<<dim3(1), dim3(kPlan), 0, s>>>(A);
+  } else {
+    const int64_t rounds = rounds_of(caches->pages);
+    int32_t* counts = A.copies + 4 + caches->pages + 1;
+    count_kernel<<<dim3((uint32_t)rounds), dim3(kPlan), 0, s>>>(refs, counts, A.pages, A.vec);
+    compact_round_kernel<<<dim3((uint32_t)rounds), dim3(kPlan), 0, s>>>(A, counts);
+    move_counts_kernel<<<dim3((uint32_t)((caches->pages / 2 + kThreads - 1) / kThreads)), dim3(kThreads), 0, s>>>(A);
+  }
   launch_copies<true>(caches, count, A.copies, caches->pages / 2, table, where, batch * width, s);
 }
 

@@ -150,7 +150,7 @@ void launch_paged_attention(const nvfp4_kv_cache_t& c, const void* q, int64_t q_
 // The pages' bookkeeping.  kv_reserve_items: page slots that new tokens may
 // reach.
 int64_t kv_reserve_items(int64_t tokens, int64_t batch, int64_t page, bool offsets);
-int64_t kv_reserve_bytes(int64_t items, int64_t batch);
+int64_t kv_reserve_bytes(int64_t items, int64_t batch, int64_t pages);
 int64_t kv_compact_bytes(int64_t pages);
 void launch_kv_free(int32_t* table, int64_t batch, int64_t width, const int32_t* lens, int64_t page, int64_t keep,
                     int64_t sinks, int32_t* refs, int64_t pages, hipStream_t s);

@@ -268,13 +268,13 @@ int nvfp4_kv_free(int32_t* table, int64_t batch, int64_t width, const int32_t* l
   return launched();
 }
 
-int64_t nvfp4_kv_reserve_workspace_size(int64_t tokens, int64_t batch, int64_t page) {
+int64_t nvfp4_kv_reserve_workspace_size(int64_t tokens, int64_t batch, int64_t page, int64_t pages) {
   const int st = check_page(page, 64);
   if (st != NVFP4_OK) return st;
-  if (tokens < 0 || batch < 0 || tokens > INT_MAX || batch > kMaxPositions) return NVFP4_ERR_SHAPE;
+  if (tokens < 0 || batch < 0 || pages < 0 || tokens > INT_MAX || batch > kMaxPositions || pages > INT_MAX) return NVFP4_ERR_SHAPE;
   const int64_t items = nvfp4host::kv_reserve_items(tokens, batch, page, true);
   if (items > INT_MAX) return NVFP4_ERR_SHAPE;
-  return batch == 0 ? 0 : nvfp4host::kv_reserve_bytes(items, batch);
+  return batch == 0 ? 0 : nvfp4host::kv_reserve_bytes(items, batch, pages);
 }
 
 int nvfp4_kv_reserve(const nvfp4_kv_cache_t* caches, int64_t count, int32_t* table, int64_t batch, int64_t width,
@@ -285,7 +285,7 @@ int nvfp4_kv_reserve(const nvfp4_kv_cache_t* caches, int64_t count, int32_t* tab
   const int64_t pages = caches->pages;
   st = check_table(table, batch, width, refs, pages);
   if (st != NVFP4_OK) return st;
-  const int64_t need = nvfp4_kv_reserve_workspace_size(tokens, batch, caches->page);
+  const int64_t need = nvfp4_kv_reserve_workspace_size(tokens, batch, caches->page, pages);
   if (need < 0) return (int)need;
   int64_t t;
   if (!mul_ok(width, caches->page, &t) || t > kMaxPositions) return NVFP4_ERR_SHAPE;

@@ -134,7 +134,7 @@ def kv_reserve(caches: Union[KVCache, Sequence[KVCache]], table: torch.Tensor, l
             _refuse(index, cu_q=cu_q)
         if tokens is None:
             raise ValueError("with cu_q, tokens says how many rows there are")
-    ws_bytes = _workspace("nvfp4_kv_reserve_workspace_size", tokens, batch, first._page)
+    ws_bytes = _workspace("nvfp4_kv_reserve_workspace_size", tokens, batch, first._page, pages)
     ws = torch.empty(ws_bytes, dtype=_U8, device=table.device)
     missing = torch.empty(batch, dtype=_I32, device=table.device)
     _check("nvfp4_kv_reserve", _on_device(

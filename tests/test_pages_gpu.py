@@ -293,6 +293,50 @@ def test_reserve_many_entries_and_pages():
     run_reserve(g, [[-1] for _ in range(3000)], [1] * 3000, 2000, 16)
 
 
+def test_reserve_from_pools_that_are_counted_first():
+    """Pools of more than 65536 pages: free ones in few rounds of 16384, in the last one, all over, and too few."""
+    g = torch.Generator().manual_seed(8)
+    pages = 150001
+    for free in ([3, 16383, 16384, 70000, 70001, 131072, 150000], list(range(149990, 150001)), list(range(0, 150001, 97))):
+        refs = [1] * pages
+        for p in free:
+            refs[p] = 0
+        for new in ([16 * len(free) // 2, 5], [3, 1, 16 * len(free)]):
+            run_reserve(g, [[-1] * 1600 for _ in new], new, pages, 16, new, refs[:])
+
+
+def test_compact_to_the_border_of_a_round():
+    """As many pages in use as one or two rounds have."""
+    for used in (16384, 32768, 16383, 16385):
+        g = torch.Generator().manual_seed(used)
+        pages = 50000
+        inside = sorted(torch.randperm(pages, generator=g)[:used].tolist())
+        refs = [0] * pages
+        for p in inside:
+            refs[p] = 1
+        was = make_caches(g, 1, pages, 1, 16, 64)
+        cache = nv.KVCache(*[x.to(DEV) for x in was[0]])
+        table = [inside[-5:], inside[:5]]
+        t, r = torch.tensor(table, dtype=I32, device=DEV), torch.tensor(refs, dtype=I32, device=DEV)
+        got, where = nv.kv_compact(cache, t, r)
+        want = ref_compact(table, refs)
+        assert got.item() == used == want[2] and where.tolist() == want[3]
+        assert t.tolist() == want[0] and r.tolist() == want[1]
+        check_caches([cache], was, want[4])
+
+
+def test_tables_without_entries():
+    i32 = lambda *shape: torch.zeros(shape, dtype=I32, device=DEV)  # noqa: E731
+    cache, refs = nv.KVCache.empty(4, 1, 16, 64), i32(4)
+    assert nv.kv_reserve(cache, i32(2, 0), i32(2) + 5, refs).tolist() == [0, 0]
+    assert nv.kv_reserve(cache, i32(0, 3), i32(0), refs).tolist() == []
+    nv.kv_free(i32(2, 0), i32(2), refs, 16)
+    nv.kv_free(i32(0, 2), i32(0), refs, 16)
+    none = nv.KVCache.empty(0, 1, 16, 64)
+    used, where = nv.kv_compact(none, i32(2, 3), i32(0))
+    assert used.item() == 0 and where.tolist() == [] and refs.tolist() == [0] * 4
+
+
 def test_reserve_of_a_table_that_holds_anything():
     g = torch.Generator().manual_seed(3)
     table = scattered(g, [64, 64, 64, 64, 64], 16, 6, 30)
@@ -315,7 +359,8 @@ def test_reserve_of_a_table_that_holds_anything():
 @pytest.mark.parametrize("pages,filled,layers,heads,page,dim", [
     (1, 0.0, 1, 1, 16, 64), (1, 1.0, 1, 1, 16, 64), (17, 0.5, 2, 3, 16, 64), (100, 0.9, 1, 2, 64, 192), (64, 1.0, 1, 1, 32, 64),
     (64, 0.0, 1, 1, 32, 64), (333, 0.3, 3, 1, 128, 128), (50, 0.6, 40, 1, 16, 64), (16384, 0.5, 1, 1, 16, 64),
-    (16385, 0.7, 1, 1, 16, 64), (40007, 0.2, 1, 1, 16, 64), (60, 0.5, 1, 5, 256, 256),
+    (16385, 0.7, 1, 1, 16, 64), (40007, 0.2, 1, 1, 16, 64), (60, 0.5, 1, 5, 256, 256), (49152, 0.9, 1, 1, 16, 64),
+    (32768, 1.0, 1, 1, 16, 64), (32768, 0.0, 1, 1, 16, 64), (301, 0.5, 2, 3, 16, 64), (77, 0.4, 1, 3, 32, 192),
 ])
 def test_compact(pages, filled, layers, heads, page, dim):
     g = torch.Generator().manual_seed(pages)

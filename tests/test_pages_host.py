@@ -110,12 +110,13 @@ def test_nothing_to_do(lib):
 
 
 def test_workspace_sizes(lib):
-    assert lib.nvfp4_kv_reserve_workspace_size(64, 64, 64) >= (4 + 2 * 64 + 2 * (64 + 2 * 64 // 64) + 1) * 4
-    assert lib.nvfp4_kv_reserve_workspace_size(0, 0, 64) == 0
-    assert lib.nvfp4_kv_reserve_workspace_size(-1, 1, 64) == SHAPE
-    assert lib.nvfp4_kv_reserve_workspace_size(1, -1, 64) == SHAPE
-    assert lib.nvfp4_kv_reserve_workspace_size((1 << 31) - 1, 1 << 30, 16) == SHAPE
-    assert lib.nvfp4_kv_reserve_workspace_size(1, 1, 63) == UNSUP
+    size = lib.nvfp4_kv_reserve_workspace_size
+    assert size(64, 64, 64, 100) >= (4 + 2 * 64 + 2 * (64 + 2 * 64 // 64) + 1) * 4
+    assert size(64, 64, 64, 1 << 24) >= size(64, 64, 64, 100) + 4 * (1 << 24) // 16384 - 256
+    assert size(0, 0, 64, 8) == 0
+    assert size(-1, 1, 64, 8) == size(1, -1, 64, 8) == size(1, 1, 64, -1) == size(1, 1, 64, 1 << 31) == SHAPE
+    assert size((1 << 31) - 1, 1 << 30, 16, 8) == SHAPE
+    assert size(1, 1, 63, 8) == UNSUP
     assert lib.nvfp4_kv_compact_workspace_size(1000) >= 4016
     assert lib.nvfp4_kv_compact_workspace_size(-1) == SHAPE
     assert lib.nvfp4_kv_compact_workspace_size(1 << 31) == SHAPE
