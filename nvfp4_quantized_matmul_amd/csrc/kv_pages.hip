@@ -8,6 +8,12 @@
 //
 // Contents move as whole pages, copied for all layers' caches by one launch
 // whose pairs (from, to) the launch before it has left in the workspace.
+//
+// Small calls are the host's (5 us a call with one launch, 12 with two) and a
+// chain of a few dependent loads: freeing 2.7 us (16 sequences of 469 entries),
+// 6.0 where 64 of 256 sequences of up to 2048 entries end; forking 4.0 and 7.7
+// (128 beams of 2048 entries); reserving for 64 sequences 5.2 and the copying
+// launch that finds nothing to copy 1.9.
 #include <algorithm>
 #include <climits>
 
@@ -25,7 +31,10 @@ constexpr int kCells = 4 * kThreads;
 // those of a round of all of them.
 constexpr int kPlan = 1024, kScan = 16, kRound = kPlan * kScan;
 // Pools of more pages than these are counted by a launch of many blocks before
-// they are planned: one block takes 1.5 us a round.
+// they are planned: one block takes 1.5 us a round of a reserve, and 15 of a
+// compaction.  (Calls: a reserve from the end of 65536 pages 21 us either way, of
+// 1048576 23 us, 136 by one block; half of 65536 pages of 2 KB compacted 41 us
+// and 100.)
 constexpr int64_t kReserveAlone = 4 * kRound, kCompactAlone = kRound;
 // Bytes of a page's side that a block copies at a time, in 16-byte accesses.
 constexpr int kVecs = 4, kPiece = kVecs * kThreads * 16;

@@ -9,6 +9,8 @@ A decode step calls ``kv_append`` with the projections of its new tokens,
     o = nv.paged_attention(q, cache, table, lens)
     token = nv.sample(logits, u, temperature=t, top_p=p)
 
+(``pages.py`` has the operators that keep table and pages on the device.)
+
 As everywhere in the package the arguments' types, shapes and devices are
 checked here, the work runs in the library's HIP kernels on the current
 stream, and outputs and workspaces come from torch's allocator.
