@@ -554,7 +554,8 @@ int nvfp4_paged_attention_sinks(const nvfp4_kv_cache_t* cache, const void* q, in
  * count:
  *
  *   table  int32 [batch, width]: the pages of each sequence, in order; an entry
- *          outside [0, pages) names none, and the calls write -1 for it
+ *          outside [0, pages) names none, and stays or is copied as it is;
+ *          entries that are cleared become -1
  *   refs   int32 [pages]: the entries of the table that name a page; a page
  *          whose count is not above 0 is free.  The caller may count references
  *          of its own.
@@ -564,7 +565,8 @@ int nvfp4_paged_attention_sinks(const nvfp4_kv_cache_t* cache, const void* q, in
  * the new tokens' pages, then the append and the attention of each layer.  Like
  * those the calls read table, lens and offsets on the device only, stay inside
  * the buffers whatever they hold, and give the same results every time.  The
- * buffers of a call must not overlap.  A table has at most 2^31 - 1 entries.
+ * buffers of a call must not overlap.  A table has at most 2^31 - 1 entries, a
+ * cache whose pages are copied at most 2^19 heads.
  */
 
 /*

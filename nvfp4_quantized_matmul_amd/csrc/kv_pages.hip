@@ -345,14 +345,17 @@ __device__ __forceinline__ void plan_round(const CompactArgs& A, int64_t round, 
     if ((inside >> i) & 1) A.where[p + i] = (empty >> i) & 1 ? -1 : (int32_t)(p + i);
   int sum;   // a round has at most 2^14 of each
   const int before = block_scan(__popc(hole) | (__popc(mover) << 16), shared, &sum);
-  for (int k = *holes + (before & 0xffff); hole; hole &= hole - 1, ++k) A.copies[5 + 2 * (int64_t)k] = (int32_t)(p + __builtin_ctz(hole));
-  for (int k = *movers + (before >> 16); mover; mover &= mover - 1, ++k) A.copies[4 + 2 * (int64_t)k] = (int32_t)(p + __builtin_ctz(mover));
+  // (k stays in the list also if another stream changes the counts meanwhile)
+  const int room = A.pages / 2;
+  for (int k = *holes + (before & 0xffff); hole && k < room; hole &= hole - 1, ++k) A.copies[5 + 2 * (int64_t)k] = (int32_t)(p + __builtin_ctz(hole));
+  for (int k = *movers + (before >> 16); mover && k < room; mover &= mover - 1, ++k) A.copies[4 + 2 * (int64_t)k] = (int32_t)(p + __builtin_ctz(mover));
   *holes += sum & 0xffff;
   *movers += sum >> 16;
 }
 
 __device__ __forceinline__ void move_count(const CompactArgs& A, int64_t k) {
   const int32_t from = A.copies[4 + 2 * k], to = A.copies[5 + 2 * k];
+  if (!is_page(from, A.pages) || !is_page(to, A.pages)) return;
   A.where[from] = to;
   A.refs[to] = A.refs[from];
   A.refs[from] = 0;
@@ -373,6 +376,7 @@ __global__ __launch_bounds__(kPlan) void compact_kernel(CompactArgs A) {
   int holes = 0, movers = 0;
   for (int64_t r = 0; r < rounds; ++r) plan_round(A, r, used, &holes, &movers, shared);
   __syncthreads();
+  movers = movers < A.pages / 2 ? movers : A.pages / 2;
   for (int k = tid; k < movers; k += kPlan) move_count(A, k);
   if (tid == 0) {
     A.copies[0] = movers;
@@ -400,7 +404,7 @@ __global__ __launch_bounds__(kPlan) void compact_round_kernel(CompactArgs A, con
   int holes = mine <= border ? free_before : all;
   int movers = mine <= border ? 0 : mine * kRound - free_before - (used - all);
   if (mine == 0 && threadIdx.x == 0) {
-    A.copies[0] = all;
+    A.copies[0] = all < A.pages / 2 ? all : A.pages / 2;
     *A.used = used;
   }
   plan_round(A, mine, used, &holes, &movers, shared);
@@ -457,6 +461,7 @@ __global__ __launch_bounds__(kThreads) void copy_kernel(CopyArgs A) {
     const int64_t from0 = A.copies[4 + 2 * (int64_t)pair0], to0 = A.copies[5 + 2 * (int64_t)pair0];
     u32x4_t x[kVecs];
     if constexpr (!GROUPED) {
+      if (!is_page((int32_t)from0, A.pages) || !is_page((int32_t)to0, A.pages)) continue;
       const u32x4_t* src = (const u32x4_t*)(base + from0 * A.page_bytes);
       u32x4_t* dst = (u32x4_t*)(base + to0 * A.page_bytes);
       const uint32_t v = piece * (kPiece / 16) + threadIdx.x;
@@ -474,6 +479,7 @@ __global__ __launch_bounds__(kThreads) void copy_kernel(CopyArgs A) {
         dst[i] = nullptr;
         if (local < group && pair < count) {
           const int64_t from = A.copies[4 + 2 * (int64_t)pair], to = A.copies[5 + 2 * (int64_t)pair];
+          if (!is_page((int32_t)from, A.pages) || !is_page((int32_t)to, A.pages)) continue;
           const u32x4_t* src = (const u32x4_t*)(base + from * A.page_bytes) + off;
           dst[i] = (u32x4_t*)(base + to * A.page_bytes) + off;
           x[i] = ONCE ? __builtin_nontemporal_load(src) : *src;
@@ -488,7 +494,7 @@ __global__ __launch_bounds__(kThreads) void copy_kernel(CopyArgs A) {
         const uint32_t local = GROUPED ? h / heads : 0, pair = pair0 + local, head = h - local * heads;
         if (pair < count) {
           const int64_t from = A.copies[4 + 2 * (int64_t)pair], to = A.copies[5 + 2 * (int64_t)pair];
-          scales[to * heads + head] = scales[from * heads + head];
+          if (is_page((int32_t)from, A.pages) && is_page((int32_t)to, A.pages)) scales[to * heads + head] = scales[from * heads + head];
         }
       }
     }

@@ -27,6 +27,9 @@ constexpr int64_t kMaxPositions = 1LL << 30;
 // each, in a 32-bit index.
 constexpr int64_t kMaxTurnedHeads = 1LL << 20;
 
+// A page that is copied has its 16-byte parts counted in 32 bits, up to 4096 a head.
+constexpr int64_t kMaxPageHeads = 1LL << 19;
+
 // Elements from the first to behind the last one of [tokens, heads, dim] with
 // these strides.
 bool extent(int64_t tokens, int64_t heads, int64_t dim, int64_t ts, int64_t hs, int64_t* n) {
@@ -90,6 +93,7 @@ int check_caches(const nvfp4_kv_cache_t* c, int64_t count) {
     if (c[i].pages != c->pages || c[i].heads != c->heads || c[i].page != c->page || c[i].dim != c->dim)
       return NVFP4_ERR_SHAPE;
   }
+  if (c->heads > kMaxPageHeads) return NVFP4_ERR_SHAPE;
   return NVFP4_OK;
 }
 

@@ -81,6 +81,7 @@ def test_reserve_refusals(lib, bad, status):
 def test_cache_refusals(lib, call, bad, status):
     assert call(lib, c=caches(3, **bad), count=3) == status
     assert call(lib, c=caches(1, k_scales=None)) == NULLPTR
+    assert call(lib, c=caches(1, heads=(1 << 19) + 1)) == SHAPE
 
 
 @pytest.mark.parametrize("bad,status", [
