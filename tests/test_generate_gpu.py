@@ -71,3 +71,49 @@ def test_samples_share_their_prompt():
 def test_a_pool_that_is_too_small():
     with pytest.raises(RuntimeError, match="too small"):
         generate.generate(PROMPTS, 70, pages=7)
+
+
+def test_a_decode_step_in_a_graph():
+    """Freeing, reserving, normed appends and attention with sinks of both layers, captured on a stream of their own and
+    replayed as lengths grow over pages, against the same steps run eagerly."""
+    n, window, sinks, width, pages = 3, 40, 3, 6, 14
+    model = generate.Decoder(DEV, norm=True, window=window, sinks=sinks)
+    start = torch.tensor([5, 60, 100], dtype=torch.int32, device=DEV)
+
+    def state():
+        return {"caches": [nv.KVCache.empty(pages, generate.KV_HEADS, generate.PAGE, generate.DIM, DEV) for _ in range(generate.LAYERS)],
+                "table": torch.full((n, width), -1, dtype=torch.int32, device=DEV),
+                "refs": torch.zeros(pages, dtype=torch.int32, device=DEV), "lens": start.clone(),
+                "tokens": torch.tensor([1, 2, 3], device=DEV)}
+
+    def prefill(s):
+        counts = start.tolist()
+        cu = torch.tensor([0, 5, 65, 165], dtype=torch.int32, device=DEV)
+        assert nv.kv_reserve(s["caches"], s["table"], s["lens"], s["refs"], cu_q=cu, tokens=165).tolist() == [0] * n
+        model(torch.arange(165, device=DEV) % 97, s["caches"], s["table"], s["lens"], cu_q=cu, max_q=max(counts))
+
+    def step(s):
+        s["lens"].add_(1)
+        nv.kv_free(s["table"], s["lens"], s["refs"], generate.PAGE, keep=window, sinks=sinks)
+        missing = nv.kv_reserve(s["caches"], s["table"], s["lens"], s["refs"])
+        x = model(s["tokens"], s["caches"], s["table"], s["lens"])
+        s["tokens"].add_(1)
+        return x, missing
+
+    eager, captured = state(), state()
+    prefill(eager), prefill(captured)
+    warm = state()
+    prefill(warm), step(warm)
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=stream):
+        got, missing = step(captured)
+    for i in range(150):
+        graph.replay()
+        torch.cuda.synchronize()
+        want, _ = step(eager)
+        assert torch.equal(got, want) and missing.tolist() == [0] * n, i
+        assert torch.equal(captured["table"], eager["table"]) and torch.equal(captured["refs"], eager["refs"]), i
+    for a, b in zip(captured["caches"], eager["caches"]):
+        assert torch.equal(a.k, b.k) and torch.equal(a.v, b.v)
+    assert (eager["refs"] > 0).sum() <= n * 3          # sinks, and the one or two pages of a window

@@ -199,6 +199,25 @@ def test_unit_weights_leave_normed_rows_to_the_plain_append(dtype, interleaved):
     assert torch.equal(caches[0].v, caches[1].v) and torch.equal(caches[0].v, caches[2].v)
 
 
+def test_rows_of_no_sequence():
+    """Rows behind the last sequence: queries are normed and stay where they are, keys go nowhere."""
+    g = torch.Generator().manual_seed(11)
+    for dtype, tokens in ((BF16, 30), (F32, 1300)):
+        q, k = torch.randn(tokens, 3, 64, generator=g).to(dtype), torch.randn(tokens, 1, 64, generator=g).to(dtype)
+        w = 1.0 + 0.3 * torch.randn(64, generator=g)
+        inv = 10000.0 ** (-torch.arange(0, 64, 2).float() / 64)
+        cache = nv.KVCache.empty(4, 1, 16, 64)
+        out, guard = guarded((tokens, 3, 64), dtype)
+        nv.kv_append(k.to(DEV), k.to(DEV), cache, i32([[2, 1], [0, 3]]), i32([20, 9]), q=q.to(DEV), cu_q=i32([0, 11, 13]),
+                     max_q=11, inv_freq=inv.to(DEV), q_norm=w.to(DEV), k_norm=w.to(DEV), out=out)
+        guard()
+        pos = torch.cat((torch.arange(9, 20), torch.arange(7, 9), torch.zeros(tokens - 13, dtype=torch.long)))
+        want = turned(normed(q, w, 1e-6), pos, inv, False).float().to(dtype)
+        ulps = 0.0 if dtype != F32 else 2.0 ** -23
+        assert ((out.cpu().double() - want.double()).abs() <= ulps * want.double().abs()).all()
+        assert (cache.k[3] == 0).all() and (cache.k[1, :, 4:] == 0).all() and (cache.k[0, :, 9:] == 0).all()
+
+
 def test_refusals():
     z = lambda *s, t=BF16: torch.zeros(s, dtype=t, device=DEV)  # noqa: E731
     cache = nv.KVCache.empty(2, 2, 16, 64)
