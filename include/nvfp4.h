@@ -591,7 +591,8 @@ int nvfp4_kv_free(int32_t* table, int64_t batch, int64_t width, const int32_t* l
  * need one in the order of (sequence, entry); counts become 1, those of shared
  * pages fall by one.  Where earlier tokens of the sequence share a page with
  * new ones its contents are copied, in all caches; the contents of other pages
- * are not changed.
+ * are not changed.  Tokens behind the table's width have no entry and are left
+ * out, as by the append.
  *
  * missing int32 [batch]: 0, or the pages that a sequence needs where they, with
  * those of the sequences before it, are more than there are free ones: then

@@ -1125,7 +1125,7 @@ struct Plan {
 // time by what was measured at 128 channels.  A tile takes a block 1.9 us where
 // it has its unit to itself, 2.5 where two share one; splits cost 8 us, and
 // their partial sums, written and read, go at 4 TB/s.  (42 heads of 128 over 6,
-// 768 new tokens: 16 tiles 44 us whole and 59 halved, 66 tiles 127 and 115; 18
+// 768 new tokens: 20 tiles 44 us whole and 59 halved, 68 tiles 127 and 115; 18
 // new tokens 75 whole, 28 in four.)
 int64_t many_splits(int64_t tiles, int64_t base, int64_t most, int64_t dim) {
   int64_t best = 1;

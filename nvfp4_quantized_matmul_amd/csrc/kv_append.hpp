@@ -335,7 +335,7 @@ __device__ __forceinline__ int row_position(const AppendArgs& A, int t) {
 namespace nvfp4host {
 
 // The append with norms; `vec`: 16-byte accesses of q, k and v.  _blocks: its
-// grid, in blocks of 256 threads, with page_blocks for the pages.
+// grid, with page_blocks for the pages.
 int64_t kv_append_norm_blocks(int64_t page_blocks, int64_t page, int64_t dim, int64_t heads_q, int64_t tokens, int64_t max_q);
 void launch_kv_append_norm(const nvfp4dev::AppendArgs& A, nvfp4_dtype_t dt, bool vec, bool inter, int64_t max_q, hipStream_t s);
 

@@ -8,19 +8,17 @@
 // 32 bits once, behind its rotation.
 //
 // A head's row lies with a group of lanes that sum their squares among
-// themselves, 8 channels of a key or 16 of a query a lane.  Sines and cosines are formed by all lanes
-// together into LDS, which keeps the code short: what a small call waits for is
-// its instructions, read once.  Blocks are of as many threads as have work.
+// themselves, 8 channels of a key or 16 of a query a lane.  Sines and cosines
+// are formed by all lanes together into LDS, which keeps the code short: what a
+// small call waits for is its instructions, read once.
 //
 // Decode batch: bound by its chain of loads and 64-bit operations, 6.6 us (64
 // sequences, 32 + 2 x 8 heads of 128; 25 us in blocks of 256 threads with 16
 // channels a lane and angles formed by each, whose 190 registers left two waves
 // a SIMD).  Prompts: bound by memory and, close behind, by the vector units'
 // 64-bit operations: three ragged prompts of up to 4096 tokens, 32 + 2 x 8 heads
-// of 128 in bf16 (207 MB) 55 us, 3.8 TB/s; 42 + 2 x 6 heads in f16 with a weight
-// for each head and a rotation of 96 channels (272 MB) 82 us, 3.3 TB/s, and 74
-// on inputs that the last-level cache partly holds, where the append without
-// norms takes 64.
+// of 128 in bf16 (207 MB) 54 us, 3.8 TB/s; 42 + 2 x 6 heads in f16 with a weight
+// for each head and a rotation of 96 channels (272 MB) 80 us, 3.4 TB/s.
 #include <algorithm>
 #include <climits>
 
@@ -32,8 +30,7 @@ namespace {
 using namespace nvfp4dev;
 
 // Rounds of a page's keys that stay in registers between the two passes over
-// it; what is over is formed twice.  (Two rounds in blocks of up to 1024 threads
-// took that prompt 100 us instead of 89.)
+// it; what is over is formed twice.
 constexpr int kHeld = 4;
 
 // W = 8, 4 or 1 consecutive elements as they are loaded.
@@ -398,9 +395,12 @@ __global__ __launch_bounds__(THREADS) void norm_append_kernel(AppendArgs A, int 
                                  A.c.vs + p.ph, p.pos0, p.begin, p.end, shared);
 }
 
-// Blocks of as many threads as the rows of a page that new tokens can fill keep
-// busy for kHeld rounds.  In blocks of one wave, for few tokens, a token's
-// queries go in parts of one round.
+// Blocks of 256 threads, or of one wave where the rows of a page that new
+// tokens can fill are two rounds of it at most; then a token's queries go in
+// parts of one round.  (Blocks of 512 threads hold pages of 16384 values for the
+// second pass, where 256 form half of them again: three prompts of up to 4096
+// tokens in pages of 128, 42 + 2 x 6 heads of 128, 85 us with them and 80
+// without, in bf16 with shared weights 59 and 55, in float32 81 and 77.)
 struct Plan {
   int threads;
   int64_t q_heads, q_parts, q_blocks;
@@ -409,8 +409,7 @@ template <int W>
 Plan make_plan(int64_t page, int64_t dim, int64_t heads_q, int64_t tokens, int64_t max_q) {
   Plan p;
   const int lanes = Row<float, W, false>::group((int)dim);
-  const int64_t rows = (max_q < page ? max_q : page) * lanes;
-  p.threads = rows <= 64 * kHeld / 2 ? 64 : rows <= 256 * kHeld ? 256 : 512;
+  p.threads = (max_q < page ? max_q : page) * lanes <= 2 * 64 ? 64 : 256;
   p.q_heads = p.threads == 64 && tokens <= 256 ? 64 / Row<float, W == 1 ? 1 : 8, false>::group((int)dim) : heads_q;
   p.q_parts = heads_q ? (heads_q + p.q_heads - 1) / p.q_heads : 0;
   const int64_t waves = p.threads / 64;
@@ -426,11 +425,8 @@ void launch_threads(const AppendArgs& A, const Plan& p, hipStream_t s) {
 template <typename T, int W, bool INTER>
 void launch(const AppendArgs& A, int64_t max_q, hipStream_t s) {
   const Plan p = make_plan<W>(1 << A.c.page_shift, A.dim, A.heads_q, A.s.tokens, max_q);
-  switch (p.threads) {
-    case 64: launch_threads<T, W, INTER, 64>(A, p, s); break;
-    case 256: launch_threads<T, W, INTER, 256>(A, p, s); break;
-    default: launch_threads<T, W, INTER, 512>(A, p, s); break;
-  }
+  if (p.threads == 64) launch_threads<T, W, INTER, 64>(A, p, s);
+  else launch_threads<T, W, INTER, 256>(A, p, s);
 }
 
 template <typename T>
@@ -445,8 +441,7 @@ namespace nvfp4host {
 
 int64_t kv_append_norm_blocks(int64_t page_blocks, int64_t page, int64_t dim, int64_t heads_q, int64_t tokens, int64_t max_q) {
   const Plan a = make_plan<4>(page, dim, heads_q, tokens, max_q), b = make_plan<1>(page, dim, heads_q, tokens, max_q);
-  const auto blocks = [&](const Plan& p) { return (page_blocks + p.q_blocks) * std::max<int64_t>(p.threads / 256, 1); };
-  return std::max(blocks(a), blocks(b));
+  return page_blocks + std::max(a.q_blocks, b.q_blocks);
 }
 
 void launch_kv_append_norm(const nvfp4dev::AppendArgs& A, nvfp4_dtype_t dt, bool vec, bool inter, int64_t max_q, hipStream_t s) {

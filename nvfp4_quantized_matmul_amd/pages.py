@@ -116,10 +116,11 @@ def kv_reserve(caches: Union[KVCache, Sequence[KVCache]], table: torch.Tensor, l
     rows and `tokens` how many rows there are (default: one token for each
     sequence).  An entry that new tokens reach gets a free page, the lowest
     first, where it names none or one that is named more than once: then its
-    contents are copied in all caches if earlier tokens share the page.  A
-    sequence whose pages, with those of the sequences before it, are more than
-    are free keeps its entries as they are; no token may be appended to it
-    before a later call has served it.
+    contents are copied in all caches if earlier tokens share the page.  Tokens
+    behind the table's width have no entry and are left out.  A sequence whose
+    pages, with those of the sequences before it, are more than are free keeps
+    its entries as they are; no token may be appended to it before a later call
+    has served it.
     """
     index, batch, width, pages = _table(table, lens, refs)
     first, count, structs = _layers(caches, index, pages)
