@@ -134,7 +134,9 @@ CASES = [
     (F32, 1, 1, 64, 16, [100000], [3], 64, False),
     (F16, 5, 1, 192, 16, [2, 30], [17, 64], 192, False),
     (BF16, 3, 1, 256, 256, [0], [256], 0, True),
-    (BF16, 4, 1, 64, 64, [9], [1100], 64, False),             # more than 1024 tokens: four a block of queries
+    (BF16, 4, 1, 64, 64, [9], [1100], 64, False),
+    (F32, 1, 1, 64, 256, [60000], [300], 64, False),          # angles of far positions, turned on over eight rounds
+    (F16, 2, 1, 128, 256, [20003], [400], 96, True),
 ]
 
 
