@@ -86,25 +86,29 @@ def generate(prompts, steps, temperature=0.8, top_k=50, top_p=0.95, seed=1, devi
     ends = torch.tensor(counts).cumsum(0)
     cu = torch.cat((torch.zeros(1, dtype=torch.int64), ends)).int().to(device)
     lens = torch.tensor(counts, dtype=torch.int32, device=device)
-    missing = nv.kv_reserve(caches, table, lens, refs, cu_q=cu, tokens=sum(counts)).amax()
+    small = f"the pool of {pages} pages was too small"
+    if nv.kv_reserve(caches, table, lens, refs, cu_q=cu, tokens=sum(counts)).any():
+        raise RuntimeError(small)
     x = model(torch.tensor(sum(prompts, []), device=device), caches, table, lens, cu_q=cu, max_q=max(counts))
     x = x[(ends - 1).to(device)]
     if samples > 1:
         parent = torch.arange(len(prompts), dtype=torch.int32, device=device).repeat_interleave(samples)
         table, lens = nv.kv_fork(table, lens, refs, parent)
         x = x[parent.long()]
-    out = []
+    out, waited = [], torch.zeros(n, dtype=torch.bool, device=device)
     for i in range(steps):
         out.append(nv.sample(nv.qmm(x, *model.head), u[i], **settings))
         if i + 1 < steps:
             lens = lens + 1
             if window > 0:
                 nv.kv_free(table, lens, refs, PAGE, keep=window, sinks=sinks)
-            missing = torch.maximum(missing, nv.kv_reserve(caches, table, lens, refs).amax())
-            x = model(out[-1], caches, table, lens)
-    # read once, at the end: a server would look before each step, and let sequences wait
-    if missing.item() > 0:
-        raise RuntimeError(f"the pool of {pages} pages was too small")
+            # who got no pages waits: with length 0 its token goes nowhere, and the step comes again
+            waits = nv.kv_reserve(caches, table, lens, refs) > 0
+            x = torch.where(waits[:, None], x, model(out[-1], caches, table, torch.where(waits, 0, lens)))
+            lens, waited = lens - waits.int(), waited | waits
+    # read once, at the end: who waited has fewer tokens than steps
+    if waited.any():
+        raise RuntimeError(small)
     return torch.stack(out, 1)
 
 

@@ -562,11 +562,12 @@ int nvfp4_paged_attention_sinks(const nvfp4_kv_cache_t* cache, const void* q, in
  *
  * A new table is all -1 with counts 0.  A decode step that moves on in lens
  * calls nvfp4_kv_free for what it no longer needs, then nvfp4_kv_reserve for
- * the new tokens' pages, then the append and the attention of each layer.  Like
- * those the calls read table, lens and offsets on the device only, stay inside
- * the buffers whatever they hold, and give the same results every time.  The
- * buffers of a call must not overlap.  A table has at most 2^31 - 1 entries, a
- * cache whose pages are copied at most 2^19 heads.
+ * the new tokens' pages, then the append and the attention of each layer, with
+ * length 0 for the sequences that are missing pages.  Like those the calls read
+ * table, lens and offsets on the device only, stay inside the buffers whatever
+ * they hold, and give the same results every time.  The buffers of a call must
+ * not overlap.  A table has at most 2^31 - 1 entries, a cache whose pages are
+ * copied at most 2^19 heads.
  */
 
 /*
@@ -597,7 +598,9 @@ int nvfp4_kv_free(int32_t* table, int64_t batch, int64_t width, const int32_t* l
  * missing int32 [batch]: 0, or the pages that a sequence needs where they, with
  * those of the sequences before it, are more than there are free ones: then
  * all of its entries stay as they were.  No token may be appended to it before
- * a later call has served it: it may still share the page it would be written to.
+ * a later call has served it: it may still share the page it would be written
+ * to.  With 0 in its place in lens the append writes none of its tokens, and the
+ * attention gives zeros; the same tokens come again with a later step.
  *
  * workspace: device, 16-byte aligned, of at least
  * nvfp4_kv_reserve_workspace_size bytes.

@@ -9,12 +9,18 @@ with counts 0.  A decode step::
 
     lens += 1
     nv.kv_free(table, lens, refs, page, keep=window, sinks=sinks)
-    missing = nv.kv_reserve(caches, table, lens, refs)
+    waits = nv.kv_reserve(caches, table, lens, refs) > 0
+    step = torch.where(waits, 0, lens)
     for cache in caches:
-        q = nv.kv_append(k, v, cache, table, lens, q=q, inv_freq=inv_freq)
-        o = nv.paged_attention(q, cache, table, lens, window=window, sinks=sinks)
+        q = nv.kv_append(k, v, cache, table, step, q=q, inv_freq=inv_freq)
+        o = nv.paged_attention(q, cache, table, step, window=window, sinks=sinks)
+    lens -= waits.int()
 
-Nothing is read on the host, so a step can be captured in a graph.
+A sequence that got no pages must not be appended to: its entry names no page,
+or one that other sequences read too.  With length 0 its new tokens are written
+nowhere and see nothing (their rows of o are zeros); its length is taken back,
+and the same tokens come again with a later step.  Nothing is read on the host,
+so a step can be captured in a graph.
 """
 
 from __future__ import annotations
@@ -120,7 +126,7 @@ def kv_reserve(caches: Union[KVCache, Sequence[KVCache]], table: torch.Tensor, l
     behind the table's width have no entry and are left out.  A sequence whose
     pages, with those of the sequences before it, are more than are free keeps
     its entries as they are; no token may be appended to it before a later call
-    has served it.
+    has served it: give it length 0 in the calls that follow.
     """
     index, batch, width, pages = _table(table, lens, refs)
     first, count, structs = _layers(caches, index, pages)
