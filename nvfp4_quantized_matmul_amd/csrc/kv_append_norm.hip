@@ -197,8 +197,9 @@ __device__ __forceinline__ void store_finite_codes(uint8_t* row, int c, const fl
 
 // Angles: the first round's sines and cosines are formed by all threads into
 // LDS, and those of the step from a round to the next.  Each lane takes its
-// pairs' into registers and turns them on from round to round, which adds 2^-52
-// or so each time.
+// pairs' into registers and turns them on from round to round, up to 63 times:
+// that adds 2^-52 or so each time, since the step has sums of two more terms
+// (with those of the first round, off by up to 4e-13, each turn would add that).
 template <typename T, int W, bool INTER, int THREADS>
 __device__ void norm_keys(const AppendArgs& A, const T* k, const float* norm, uint8_t* codes, uint8_t* scale, int pos0,
                           int begin, int end, double2* turn, double2* step, uint32_t* shared) {
@@ -226,7 +227,7 @@ __device__ void norm_keys(const AppendArgs& A, const T* k, const float* norm, ui
   if (each < tokens) {
     for (int f = threadIdx.x; f < half; f += THREADS) {
       double sn, cs;
-      sin_cos((double)each * (double)A.inv_freq[f], &sn, &cs);
+      sin_cos<true>((double)each * (double)A.inv_freq[f], &sn, &cs);
       step[f] = make_double2(sn, cs);
     }
   }
