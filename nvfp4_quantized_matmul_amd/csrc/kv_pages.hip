@@ -322,7 +322,7 @@ __global__ __launch_bounds__(kPlan) void reserve_kernel(ReserveArgs A) {
 }
 
 // ---------------------------------------------------------------------------
-// compacting: one block plans, or a block each round
+// compacting: a block plans each round, alone for a pool of one
 // ---------------------------------------------------------------------------
 
 struct CompactArgs {
@@ -332,13 +332,12 @@ struct CompactArgs {
   bool vec;
 };
 
-// The round's part of the plan: holes are the free pages below `used`, movers
-// the pages in use from there on; `holes` and `movers` count those of earlier
-// rounds.
-__device__ __forceinline__ void plan_round(const CompactArgs& A, int64_t round, int used, int* holes, int* movers, int* shared) {
-  const int64_t p = round * kRound + threadIdx.x * kScan;
+// The round's part of the plan, of the thread's pages from p on, those in
+// `empty` free: holes are the free pages below `used`, movers the pages in use
+// from there on; `holes` and `movers` are those of earlier rounds.  Gives the
+// movers of this round and earlier ones.
+__device__ __forceinline__ int plan_round(const CompactArgs& A, int64_t p, uint32_t empty, int used, int holes, int movers, int* shared) {
   const uint32_t inside = pages_below(p, A.pages), low = pages_below(p, used);
-  const uint32_t empty = free_pages(A.refs, p, A.pages, A.vec) & inside;
   uint32_t hole = empty & low, mover = inside & ~empty & ~low;
 #pragma unroll
   for (int i = 0; i < kScan; ++i)
@@ -347,10 +346,9 @@ __device__ __forceinline__ void plan_round(const CompactArgs& A, int64_t round, 
   const int before = block_scan(__popc(hole) | (__popc(mover) << 16), shared, &sum);
   // (k stays in the list also if another stream changes the counts meanwhile)
   const int room = A.pages / 2;
-  for (int k = *holes + (before & 0xffff); hole && k < room; hole &= hole - 1, ++k) A.copies[5 + 2 * (int64_t)k] = (int32_t)(p + __builtin_ctz(hole));
-  for (int k = *movers + (before >> 16); mover && k < room; mover &= mover - 1, ++k) A.copies[4 + 2 * (int64_t)k] = (int32_t)(p + __builtin_ctz(mover));
-  *holes += sum & 0xffff;
-  *movers += sum >> 16;
+  for (int k = holes + (before & 0xffff); hole && k < room; hole &= hole - 1, ++k) A.copies[5 + 2 * (int64_t)k] = (int32_t)(p + __builtin_ctz(hole));
+  for (int k = movers + (before >> 16); mover && k < room; mover &= mover - 1, ++k) A.copies[4 + 2 * (int64_t)k] = (int32_t)(p + __builtin_ctz(mover));
+  return movers + (sum >> 16);
 }
 
 __device__ __forceinline__ void move_count(const CompactArgs& A, int64_t k) {
@@ -361,20 +359,15 @@ __device__ __forceinline__ void move_count(const CompactArgs& A, int64_t k) {
   A.refs[from] = 0;
 }
 
+// Pools of one round at most.
 __global__ __launch_bounds__(kPlan) void compact_kernel(CompactArgs A) {
   __shared__ int shared[kPlan / 64];
   const int tid = threadIdx.x;
-  const int64_t rounds = ((int64_t)A.pages + kRound - 1) / kRound;
-  int used = 0;
-  for (int64_t r = 0; r < rounds; ++r) {
-    const int64_t p = r * kRound + tid * kScan;
-    used += __popc(pages_below(p, A.pages)) - __popc(free_pages(A.refs, p, A.pages, A.vec));
-  }
-  int all;
-  block_scan(used, shared, &all);
-  used = all;
-  int holes = 0, movers = 0;
-  for (int64_t r = 0; r < rounds; ++r) plan_round(A, r, used, &holes, &movers, shared);
+  const int64_t p = tid * kScan;
+  const uint32_t empty = free_pages(A.refs, p, A.pages, A.vec);
+  int used;
+  block_scan(__popc(pages_below(p, A.pages)) - __popc(empty), shared, &used);
+  int movers = plan_round(A, p, empty, used, 0, 0, shared);
   __syncthreads();
   movers = movers < A.pages / 2 ? movers : A.pages / 2;
   for (int k = tid; k < movers; k += kPlan) move_count(A, k);
@@ -401,13 +394,14 @@ __global__ __launch_bounds__(kPlan) void compact_round_kernel(CompactArgs A, con
   block_scan(__popc(free_pages(A.refs, p, A.pages, A.vec) & pages_below(p, used)), shared, &in_border);
   const int all = sum_to(border < rounds ? border : rounds) + in_border, free_before = sum_to(mine);
   // the movers before this round: pages in use before it but for those below `used`
-  int holes = mine <= border ? free_before : all;
-  int movers = mine <= border ? 0 : mine * kRound - free_before - (used - all);
+  const int holes = mine <= border ? free_before : all;
+  const int movers = mine <= border ? 0 : mine * kRound - free_before - (used - all);
   if (mine == 0 && threadIdx.x == 0) {
     A.copies[0] = all < A.pages / 2 ? all : A.pages / 2;
     *A.used = used;
   }
-  plan_round(A, mine, used, &holes, &movers, shared);
+  const int64_t at = (int64_t)mine * kRound + threadIdx.x * kScan;
+  plan_round(A, at, free_pages(A.refs, at, A.pages, A.vec), used, holes, movers, shared);
 }
 
 __global__ __launch_bounds__(kThreads) void move_counts_kernel(CompactArgs A) {
