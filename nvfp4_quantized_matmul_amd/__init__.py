@@ -209,7 +209,7 @@ def _qmm_workspace_bytes(lib, dev: torch.device, M: int, K: int, N: int, tr: int
     key = (dev.index, M, K, N, tr, code, route)
     ws_bytes = _QMM_WS_CACHE.get(key)
     if ws_bytes is None:
-        ws_bytes = int(lib.nvfp4_qmm_workspace_size(M, K, N, tr, code, route))
+        ws_bytes = int(_on_device(dev.index, lib.nvfp4_qmm_workspace_size, M, K, N, tr, code, route))
         if ws_bytes < 0:
             raise NVFP4Error("nvfp4_qmm_workspace_size", ws_bytes)
         if len(_QMM_WS_CACHE) < 4096:
@@ -273,8 +273,8 @@ def transcode(weight: torch.Tensor, weight_scale: torch.Tensor,
     gs = None
     if weight_scale_2 is not None:
         gs = torch.empty(batch, dtype=torch.float32, device=dev)
-    _check("nvfp4_transcode", lib.nvfp4_transcode(
-        _ptr(weight), _ptr(weight_scale), _ptr(weight_scale_2), batch, rows, cols,
+    _check("nvfp4_transcode", _on_device(
+        dev.index, lib.nvfp4_transcode, _ptr(weight), _ptr(weight_scale), _ptr(weight_scale_2), batch, rows, cols,
         _ptr(w_out), _ptr(s_out), _ptr(gs), _stream(dev)))
     return w_out, s_out, gs
 
@@ -297,8 +297,9 @@ def dequantize(w: torch.Tensor, scales: torch.Tensor, gs: Optional[torch.Tensor]
     dev = _require_gpu(w, scales, gs)
     lib = load_library()
     out = torch.empty(lead + (rows, cols), dtype=dtype, device=dev)
-    _check("nvfp4_dequantize", lib.nvfp4_dequantize(
-        _ptr(w), _ptr(scales), _ptr(gs), batch, rows, cols, code, _ptr(out), _stream(dev)))
+    _check("nvfp4_dequantize", _on_device(
+        dev.index, lib.nvfp4_dequantize, _ptr(w), _ptr(scales), _ptr(gs), batch, rows, cols, code, _ptr(out),
+        _stream(dev)))
     return out
 
 
@@ -323,8 +324,9 @@ def quantize(w: torch.Tensor, gs: Optional[torch.Tensor] = None
     w_out = torch.empty(lead + (rows, cols // 8), dtype=torch.int32, device=dev)
     s_out = torch.empty(lead + (rows, cols // 16), dtype=torch.uint8, device=dev)
     gs_out = torch.empty(batch, dtype=torch.float32, device=dev)
-    _check("nvfp4_quantize", lib.nvfp4_quantize(
-        _ptr(w), code, batch, rows, cols, _ptr(gs), _ptr(w_out), _ptr(s_out), _ptr(gs_out), _stream(dev)))
+    _check("nvfp4_quantize", _on_device(
+        dev.index, lib.nvfp4_quantize, _ptr(w), code, batch, rows, cols, _ptr(gs), _ptr(w_out), _ptr(s_out),
+        _ptr(gs_out), _stream(dev)))
     return w_out, s_out, gs_out
 
 
@@ -371,12 +373,12 @@ def qmm(x: torch.Tensor, w: torch.Tensor, scales: torch.Tensor, gs: Optional[tor
         # K-split partials or the float32 split copy live in a workspace from
         # torch's allocator (the library itself never allocates)
         ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-        _check("nvfp4_qmm_ws", lib.nvfp4_qmm_ws(
-            _ptr(x), code, M, K, N, _ptr(w), _ptr(scales), _ptr(gs), tr, _ROUTES[route],
-            _ptr(ws), ws_bytes, _ptr(out), _stream(dev)))
+        _check("nvfp4_qmm_ws", _on_device(
+            dev.index, lib.nvfp4_qmm_ws, _ptr(x), code, M, K, N, _ptr(w), _ptr(scales), _ptr(gs), tr,
+            _ROUTES[route], _ptr(ws), ws_bytes, _ptr(out), _stream(dev)))
         return out
-    _check("nvfp4_qmm", lib.nvfp4_qmm(
-        _ptr(x), code, M, K, N, _ptr(w), _ptr(scales), _ptr(gs), tr,
+    _check("nvfp4_qmm", _on_device(
+        dev.index, lib.nvfp4_qmm, _ptr(x), code, M, K, N, _ptr(w), _ptr(scales), _ptr(gs), tr,
         _ROUTES[route], _ptr(out), _stream(dev)))
     return out
 
@@ -415,13 +417,13 @@ def qmm_glu(x: torch.Tensor, w_gate: torch.Tensor, s_gate: torch.Tensor, gs_gate
     elif out.dtype != x.dtype or tuple(out.shape) != tuple(x.shape[:-1]) + (F,):
         raise ValueError("out has the wrong dtype or shape")
     _require_gpu(out)
-    ws_bytes = int(lib.nvfp4_qmm_glu_workspace_size(M, K, F, code))
+    ws_bytes = int(_on_device(dev.index, lib.nvfp4_qmm_glu_workspace_size, M, K, F, code))
     if ws_bytes < 0:
         raise NVFP4Error("nvfp4_qmm_glu_workspace_size", ws_bytes)
     ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes > 0 else None
-    _check("nvfp4_qmm_glu", lib.nvfp4_qmm_glu(
-        _ptr(x), code, M, K, F, _ptr(w_gate), _ptr(s_gate), _ptr(gs_gate), _ptr(w_up), _ptr(s_up),
-        _ptr(gs_up), _ACTS[act], _ptr(ws), ws_bytes, _ptr(out), _stream(dev)))
+    _check("nvfp4_qmm_glu", _on_device(
+        dev.index, lib.nvfp4_qmm_glu, _ptr(x), code, M, K, F, _ptr(w_gate), _ptr(s_gate), _ptr(gs_gate), _ptr(w_up),
+        _ptr(s_up), _ptr(gs_up), _ACTS[act], _ptr(ws), ws_bytes, _ptr(out), _stream(dev)))
     return out
 
 
@@ -465,12 +467,12 @@ def qmm_batched(x: torch.Tensor, w: torch.Tensor, scales: torch.Tensor,
     ws_bytes = _qmm_workspace_bytes(lib, dev, M, K, N, tr, code, _ROUTES[route]) if B > 0 else 0
     if ws_bytes > 0:
         ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-        _check("nvfp4_qmm_batched_ws", lib.nvfp4_qmm_batched_ws(
-            _ptr(x), code, XB, B, M, K, N, _ptr(w), _ptr(scales), _ptr(gs), tr, _ROUTES[route],
-            _ptr(ws), ws_bytes, _ptr(out), _stream(dev)))
+        _check("nvfp4_qmm_batched_ws", _on_device(
+            dev.index, lib.nvfp4_qmm_batched_ws, _ptr(x), code, XB, B, M, K, N, _ptr(w), _ptr(scales), _ptr(gs), tr,
+            _ROUTES[route], _ptr(ws), ws_bytes, _ptr(out), _stream(dev)))
         return out
-    _check("nvfp4_qmm_batched", lib.nvfp4_qmm_batched(
-        _ptr(x), code, XB, B, M, K, N, _ptr(w), _ptr(scales), _ptr(gs), tr,
+    _check("nvfp4_qmm_batched", _on_device(
+        dev.index, lib.nvfp4_qmm_batched, _ptr(x), code, XB, B, M, K, N, _ptr(w), _ptr(scales), _ptr(gs), tr,
         _ROUTES[route], _ptr(out), _stream(dev)))
     return out
 
@@ -508,9 +510,9 @@ def gather_qmm(x: torch.Tensor, w: torch.Tensor, scales: torch.Tensor,
     elif out.dtype != x.dtype or tuple(out.shape) != (R, M, N):
         raise ValueError("out has the wrong dtype or shape")
     _require_gpu(out)
-    _check("nvfp4_gather_qmm", lib.nvfp4_gather_qmm(
-        _ptr(x), code, X, M, K, _ptr(lhs_indices), _ptr(rhs_indices), R, _ptr(w), _ptr(scales),
-        _ptr(gs), E, N, int(bool(sorted_indices)), _ptr(out), _stream(dev)))
+    _check("nvfp4_gather_qmm", _on_device(
+        dev.index, lib.nvfp4_gather_qmm, _ptr(x), code, X, M, K, _ptr(lhs_indices), _ptr(rhs_indices), R, _ptr(w),
+        _ptr(scales), _ptr(gs), E, N, int(bool(sorted_indices)), _ptr(out), _stream(dev)))
     return out
 
 

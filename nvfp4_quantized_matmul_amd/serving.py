@@ -23,7 +23,7 @@ from typing import Optional
 
 import torch
 
-from . import _CURRENT_DEVICE, NVFP4Error, _check, _dtype_code, _stream, load_library
+from . import _CURRENT_DEVICE, NVFP4Error, _check, _dtype_code, _on_device, _stream, load_library
 
 _PAGES = (16, 32, 64, 128, 256)
 _DIMS = (64, 128, 192, 256)
@@ -375,7 +375,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Te
         if len(_SAMPLE_WS_CACHE) < 4096:
             _SAMPLE_WS_CACHE[key] = ws_bytes
     ws = torch.empty(ws_bytes, dtype=_U8, device=device) if ws_bytes else None
-    _check("nvfp4_sample", lib.nvfp4_sample(
-        logits.data_ptr(), code, batch, vocab, row, up, tp, kp, pp, mp, ws.data_ptr() if ws_bytes else None, ws_bytes,
-        token.data_ptr(), prob.data_ptr() if return_prob else None, _stream(device)))
+    _check("nvfp4_sample", _on_device(
+        index, lib.nvfp4_sample, logits.data_ptr(), code, batch, vocab, row, up, tp, kp, pp, mp,
+        ws.data_ptr() if ws_bytes else None, ws_bytes, token.data_ptr(), prob.data_ptr() if return_prob else None, _stream(device)))
     return (token, prob) if return_prob else token
