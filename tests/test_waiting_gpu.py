@@ -120,3 +120,40 @@ def test_the_example_lets_sequences_wait(monkeypatch):
     waited = torch.tensor(waits[1:]).any(0)
     assert 0 < waited.sum() < 9 and torch.tensor(waits[1]).sum() == 2
     assert torch.equal(torch.stack(tokens, 1).cpu()[~waited], want.cpu()[~waited])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 5)])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("counts", [[100, 40, 70], [1, 3, 2]])
+@pytest.mark.parametrize("width", [10, 200])                 # one share of the axis, or several
+def test_prompts_wait(counts, width, norm, window, sinks, dtype):
+    """Length 0 with new tokens: nothing of them is written, seen or changed for the others."""
+    g = torch.Generator().manual_seed(11)
+    pages, tokens = 40, sum(counts)
+    table = torch.full((3, width), -1, dtype=torch.int32)
+    table[:, :10] = torch.randperm(30, generator=g).view(3, 10).int()
+    ample = table.clone()
+    ample[1, :10] = torch.arange(30, 40)
+    table[1, :8] = table[0, :8]                               # the one that waits shares pages with the first
+    lens = i32([130, 120, 75])
+    ends = torch.tensor(counts).cumsum(0).tolist()
+    cu = i32([0] + ends)
+    codes = lambda *shape: torch.randint(0, 120, shape, generator=g).to(torch.uint8).to(DEV)  # noqa: E731
+    full = [codes(pages, KV, PAGE, DIM), codes(pages, KV, DIM, PAGE), codes(pages, KV), codes(pages, KV)]
+    rows = torch.randn(tokens, HEADS + 2 * KV, DIM, generator=g).to(dtype).to(DEV)
+    q, k, v = rows.split([HEADS, KV, KV], 1)
+    weight = {"k_norm": (1 + torch.rand(DIM, generator=g)).to(DEV)} if norm else {}
+
+    def run(table, step):
+        caches = nv.KVCache(*[t.clone() for t in full])
+        out = nv.kv_append(k, v, caches, table.to(DEV), step, q=q, cu_q=cu, max_q=max(counts), **weight)
+        return nv.paged_attention(out, caches, table.to(DEV), step, cu_q=cu, max_q=max(counts), window=window, sinks=sinks), caches
+
+    got, after = run(table, torch.where(i32([0, 1, 0]) > 0, 0, lens))
+    want, others = run(ample, lens)
+    for x, y in zip((after.k, after.v, after.k_scales, after.v_scales), (others.k, others.v, others.k_scales, others.v_scales)):
+        assert torch.equal(x[:30], y[:30])
+    waits = slice(ends[0], ends[1])
+    assert want[waits].any() and not got[waits].any()
+    assert torch.equal(got[:ends[0]], want[:ends[0]]) and torch.equal(got[ends[1]:], want[ends[1]:])
