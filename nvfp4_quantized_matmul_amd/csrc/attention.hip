@@ -214,6 +214,7 @@ __device__ __forceinline__ int32_t first_seen(const AttnArgs& A, int32_t p) {
   return A.window > 0 && p >= A.window ? p - A.window + 1 : 0;
 }
 
+template <bool SINKS>
 __device__ __forceinline__ Span span_of(const AttnArgs& A, const Sequence& s, int t0, int t1) {
   Span r;
   r.first = s.first + t0;
@@ -230,7 +231,7 @@ __device__ __forceinline__ Span span_of(const AttnArgs& A, const Sequence& s, in
   // and 264 tokens of two prompts, 42 heads over 6, 2048 + 100 seen 97 us, 612
   // TFLOP/s: 426 blocks, so that 170 units have two and 86 one.
   const int32_t front = A.sinks < r.from ? A.sinks : r.from;
-  r.begin = r.from - ((front + 63) & ~63);
+  r.begin = SINKS ? r.from - ((front + 63) & ~63) : r.from;
   return r;
 }
 
@@ -274,7 +275,8 @@ constexpr int few_lds_bytes() {
 // compiler does not always meet it: 2-byte types with 16 rows of 192 channels
 // spill 25 at two blocks (32 sequences of up to 8k tokens, 16 heads, take 38 us,
 // 41 with one block and no spill; 4 of up to 87k 199 us, and 183), 32 rows of
-// 256 spill 82, and 107 in float32, at one.
+// 256 spill 82 in bf16, 94 in f16 and 105 in float32 at one (with sinks 108, 96
+// and 109).
 constexpr int few_blocks_per_cu(int dim, int nt, int parts) { return nt * dim / 4 + 16 * nt + dim / 2 + 24 * parts * nt + 64 <= 256 ? 2 : 1; }
 
 template <typename T, int DIM, int NT, bool SINKS>
@@ -300,7 +302,9 @@ __global__ __launch_bounds__(64 * kFewWaves, few_blocks_per_cu(DIM, NT, Mma<T>::
   const int rows = sq.count * A.group, row0 = rt * ROWS;
   if (row0 >= rows) return;
   const int nrows = rows - row0 < ROWS ? rows - row0 : ROWS;
-  const Span sp = span_of(A, sq, row0 / A.group, (row0 + nrows - 1) / A.group);
+  // float32 has the sinks' form of it also without any, which spills less: 32 rows
+  // of 256 channels take 55 us with it and 58 without (bf16 44 and 43)
+  const Span sp = span_of<SINKS || PARTS == 3>(A, sq, row0 / A.group, (row0 + nrows - 1) / A.group);
   const int64_t lo64 = (int64_t)sp.begin + (int64_t)split * A.chunk;
   // a split behind the end writes nothing: the join counts the splits itself;
   // the first one always writes, so that rows that see nothing become zeros
@@ -731,7 +735,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DIM <= 64 ? 3 : DIM <= 128 ? 2 : 1
   const int rows = sq.count * A.group, row0 = rt * kManyRows;
   if (row0 >= rows) return;
   const int nrows = rows - row0 < kManyRows ? rows - row0 : kManyRows;
-  const Span sp = span_of(A, sq, row0 / A.group, (row0 + nrows - 1) / A.group);
+  const Span sp = span_of<SINKS>(A, sq, row0 / A.group, (row0 + nrows - 1) / A.group);
   const int64_t lo64 = (int64_t)sp.begin + (int64_t)split * A.chunk;
   if (split > 0 && lo64 >= sp.end) return;
   const int lo = (int)lo64;
@@ -1070,7 +1074,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs A, int rows_per_tile
   if (t < 0 || t >= sq.count) return;
   const int row = t * A.group + hh % A.group, rows = sq.count * A.group, row0 = row / rows_per_tile * rows_per_tile;
   const int last = (row0 + rows_per_tile < rows ? row0 + rows_per_tile : rows) - 1;
-  const Span sp = span_of(A, sq, row0 / A.group, last / A.group);
+  const Span sp = span_of<true>(A, sq, row0 / A.group, last / A.group);   // (sinks 0: as without)
   int n = sp.end > sp.begin ? (sp.end - sp.begin + A.chunk - 1) / A.chunk : 1;
   n = n < A.splits ? n : A.splits;
 
