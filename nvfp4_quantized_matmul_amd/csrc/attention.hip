@@ -1170,7 +1170,15 @@ Plan make_plan(int64_t heads_q, int64_t heads, int64_t page, int64_t batch, int6
     // go with a window that is short beside the sequences, spans are alike: few
     // rows then take the one round that comes nearest, and two tiles a wave (32
     // heads of 128 over 8, 4096 + 4 tokens: 64 sequences 98 us, 111 with three
-    // rounds; 16 28.7 and 36; one 11.7 and 13.8; 16 of 6 tokens 36 and 54)
+    // rounds; 16 28.7 and 36; one 11.7 and 13.8; 16 of 6 tokens 36 and 54).
+    // While sequences are shorter than the window theirs are not, and lengths
+    // are not known here: with a table of 100000 tokens 16 of up to 4096, window
+    // 4096, take 25.9 us and 23.1 with three rounds, of 6 tokens 34 and 39; 4 of
+    // up to 4096, window 8192, 17.6 and 14.4; 64 of up to 8192, window 8192, 120
+    // and 115, 32 (16 heads over 2) 25.5 and 24.4, of up to 2048 15.8 and 16.5.
+    // Windows alone keep the three rounds, so that their results stay as they
+    // are to the last bit: 64 sequences 108 us where the one round would take 99,
+    // 16 36 and 28.5, one 14.0 and 11.6, 16 of 6 tokens 53 and 37.
     const bool alike = sinks > 0 && window > 0;
     const int64_t unit = p.many ? 1 : kFewWaves, least = p.many ? 8 : (alike ? 2 : 4) * kFewWaves;
     const int64_t round = 256 * few_blocks_per_cu((int)dim, p.nt, dt == NVFP4_F32 ? 3 : 1);

@@ -12,13 +12,15 @@
 // are formed by all lanes together into LDS, which keeps the code short: what a
 // small call waits for is its instructions, read once.
 //
-// Decode batch: bound by its chain of loads and 64-bit operations, 6.6 us (64
-// sequences, 32 + 2 x 8 heads of 128; 25 us in blocks of 256 threads with 16
-// channels a lane and angles formed by each, whose 190 registers left two waves
-// a SIMD).  Prompts: bound by memory and, close behind, by the vector units'
-// 64-bit operations: three ragged prompts of up to 4096 tokens, 32 + 2 x 8 heads
-// of 128 in bf16 (207 MB) 54 us, 3.8 TB/s; 42 + 2 x 6 heads in f16 with a weight
-// for each head and a rotation of 96 channels (272 MB) 80 us, 3.4 TB/s.
+// Decode batch: bound by its chain of loads and 64-bit operations, 6.1 us in a
+// graph (64 sequences, 32 + 2 x 8 heads of 128; 25 us in blocks of 256 threads
+// with 16 channels a lane and angles formed by each, whose 190 registers left two
+// waves a SIMD).  Prompts: bound by memory and, close behind, by the vector
+// units' 64-bit operations.  Three ragged prompts of up to 4096 tokens, over four
+// sets of inputs in turn: 32 + 2 x 8 heads of 128 in bf16 (183 MB) 49 us, 3.8
+// TB/s; 42 + 2 x 6 heads (234 MB) 56; in f16 with a weight for each head and a
+// rotation of 96 channels (272 MB) 79 us, 3.4 TB/s.  Over one set, which the
+// last-level cache holds in part, 42, 50 and 71.
 #include <algorithm>
 #include <climits>
 
@@ -400,8 +402,8 @@ __global__ __launch_bounds__(THREADS) void norm_append_kernel(AppendArgs A, int 
 // tokens can fill are two rounds of it at most; then a token's queries go in
 // parts of one round.  (Blocks of 512 threads hold pages of 16384 values for the
 // second pass, where 256 form half of them again: three prompts of up to 4096
-// tokens in pages of 128, 42 + 2 x 6 heads of 128, 85 us with them and 80
-// without, in bf16 with shared weights 59 and 55, in float32 81 and 77.)
+// tokens in pages of 128, 42 + 2 x 6 heads of 128, one set of inputs, 85 us with
+// them and 80 without, in bf16 with shared weights 59 and 55, in float32 81 and 77.)
 struct Plan {
   int threads;
   int64_t q_heads, q_parts, q_blocks;
